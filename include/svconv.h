@@ -284,6 +284,128 @@ SVCONV_API int svconv_adapter_fwd_xattn(void* X, const int32_t* nbr, const int32
 SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T, int max_chunk_rows, int A);
 
 /*
+ * Cross-attention of packed groups (SV-TAD page, Key Design 3, with separate queries, keys
+ * and values, several query heads per key head, and its gradients; svconv_xattn_aux above is
+ * the form for a few queries over keys = values).  Group g owns the query rows
+ * q_off[g] .. q_off[g+1]-1 and the key rows kv_off[g] .. kv_off[g+1]-1; the two lengths are
+ * unrelated and either may be 0.  Query head h attends over key head h / (Hq / Hkv):
+ *     S[i][j] = scale * Q[i][h] . K[j][h / r]     over the group's kept keys j
+ *     P = softmax_j(S),   O[i][h] = sum_j P[i][j] V[j][h / r],   lse[i][h] = log sum_j exp(S[i][j])
+ * A row whose group has no kept key gets O = 0 and lse = -inf.  The scores, the softmax's
+ * statistics and all sums are fp32; P (and dS below) are rounded to bf16 as matrix operands.
+ *   Q [nq][Hq][d], K and V [nkv][Hkv][d] bf16 with the given row and head strides (in
+ *   elements, multiples of 8; channels contiguous), 16-byte aligned; O [nq][Hq][d] bf16 and
+ *   lse [nq][Hq] fp32, contiguous.  kv_keep [nkv] or NULL: keys with a zero byte are left out,
+ *   whatever their rows hold (infinities and NaN included).
+ *   Rows that belong to no group are neither read into a result nor written.
+ *   max_q, max_kv  upper bounds on the rows of any group; a larger group sets
+ *              SVCONV_STATUS_CHUNK_OVERFLOW and its rows past the bound are left out (not
+ *              written).  Offsets that decrease or leave 0..nq / 0..nkv set
+ *              SVCONV_STATUS_BAD_OFFSETS and that group is treated as empty (nothing written).
+ *   dev_status int32 device or NULL (then the library's error word takes the bits).
+ *   workspace  >= svconv_cross_attn_fwd_workspace_size(desc) bytes, 16-byte aligned (may be
+ *              NULL if that is 0), no initial contents required.  Calls that overlap on the GPU
+ *              (captured graphs included) need a workspace each.
+ *   Limits: d a multiple of 8, 8 <= d <= 128; Hq a multiple of Hkv, Hq / Hkv <= 128;
+ *   scale finite.  Deterministic: bitwise identical results for identical calls.
+ *
+ * svconv_cross_attn_bwd: with dO [nq][Hq][d] bf16 and O, lse of the forward call,
+ *     dP = dO V^T,  D[i] = dO[i] . O[i],  dS = P * (dP - D),
+ *     dQ = scale dS K,  dK = scale sum over the r query heads of dS^T Q,  dV = the same of P^T dO
+ *   into dQ [nq][Hq][d], dK and dV [nkv][Hkv][d] bf16 (contiguous, overwritten; rows of dropped
+ *   keys get 0).  Overlapping outputs are not allowed.  No atomics: deterministic.
+ */
+typedef struct {
+  int nq, nkv;            /* rows of Q and of K / V */
+  int Hq, Hkv, d;         /* query heads, key heads, channels per head */
+  int G;                  /* groups */
+  const int32_t* q_off;   /* [G+1] device */
+  const int32_t* kv_off;  /* [G+1] device */
+  int max_q, max_kv;      /* bounds on a group's rows */
+  const uint8_t* kv_keep; /* [nkv] device or NULL */
+  float scale;            /* usually 1 / sqrt(d) */
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head; /* strides, in elements */
+} svconv_cross_attn_desc;
+SVCONV_API int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, const void* K, const void* V,
+                                     void* O, float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                     void* stream);
+SVCONV_API size_t svconv_cross_attn_fwd_workspace_size(const svconv_cross_attn_desc* desc);
+SVCONV_API int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, const void* Q, const void* K,
+                                     const void* V, const void* O, const float* lse, void* dQ, void* dK, void* dV,
+                                     void* workspace, size_t ws_bytes, int32_t* dev_status, void* stream);
+SVCONV_API size_t svconv_cross_attn_bwd_workspace_size(const svconv_cross_attn_desc* desc);
+
+/*
+ * Per-head RMS norm of the queries and keys of svconv_cross_attn_fwd with the rotary
+ * positions of their tokens, in one pass and one launch over both.  For each token n and
+ * head h, with x = X[n][h] of d channels:
+ *     u = x / sqrt(mean(x^2) + eps) * w,
+ *     pair p of the first rot channels is turned by the angle pos[n][axis(p)] * freq[p]:
+ *     (y_a, y_b) = (u_a cos - u_b sin, u_a sin + u_b cos),   y = u for the other channels.
+ *   Pair p is (p, p + rot / 2) for SVCONV_ROPE_HALF and (2p, 2p + 1) for
+ *   SVCONV_ROPE_INTERLEAVED.  The first axis_pairs[0] pairs follow axis 0, the next
+ *   axis_pairs[1] axis 1, and so on (host array of `axes` counts that add up to rot / 2), so
+ *   the coords table of svconv_build_index, (t, y, x) per token, serves as pos with axes = 3.
+ *   freq is fp64 [rot / 2] DEVICE, radians per unit of position: any spacing or scaling for
+ *   long sequences is the caller's.  Angles are formed in fp64, so far positions lose nothing.
+ *   A side with n = 0 is skipped (its pointers may be NULL).
+ *   x [n][H][d] of dtype (SVCONV_F32 or SVCONV_BF16) with a row stride in elements (a multiple
+ *   of 8, heads contiguous); y, dy, dx [n][H][d] contiguous; pos int32 [n][axes]; w fp32 [d] or
+ *   NULL (all ones).  y may be x itself when x is contiguous (in place), and dx may be dy.
+ *   Limits: d a multiple of 8, 8 <= d <= 256; rot a multiple of 16, 0 <= rot <= d;
+ *   1 <= axes <= 3; eps >= 0; 16-byte aligned x, y, dy, dx.
+ *
+ * svconv_qk_norm_rope_bwd: dx and dw [d] fp32 (or NULL) of each side from dy, with the norm
+ *   recomputed from x.  dw sums over tokens and heads in a fixed order: deterministic.  A side
+ *   with n = 0 gets dw = 0.
+ *   workspace >= svconv_qk_norm_rope_bwd_workspace_size(d) bytes, 16-byte aligned.
+ */
+#define SVCONV_ROPE_HALF 0
+#define SVCONV_ROPE_INTERLEAVED 1
+typedef struct {
+  const void* x;
+  int64_t x_row;      /* row stride of x, in elements */
+  int n, H;
+  const int32_t* pos; /* [n][axes] device */
+  const float* w;     /* [d] device or NULL */
+  void* y;            /* forward */
+  const void* dy;     /* backward */
+  void* dx;
+  float* dw;
+} svconv_qk_side;
+SVCONV_API int svconv_qk_norm_rope_fwd(int dtype, int d, int rot, int layout, const double* freq, int axes,
+                                       const int32_t* axis_pairs, float eps, const svconv_qk_side* q,
+                                       const svconv_qk_side* k, void* stream);
+SVCONV_API int svconv_qk_norm_rope_bwd(int dtype, int d, int rot, int layout, const double* freq, int axes,
+                                       const int32_t* axis_pairs, float eps, const svconv_qk_side* q,
+                                       const svconv_qk_side* k, void* workspace, size_t ws_bytes, void* stream);
+SVCONV_API size_t svconv_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * Global norm of a set of gradients (dW and db of svconv_bwd and of the calls above) and
+ * clipping by it:
+ *     norm = sqrt(sum over all tensors of g^2),  dst = g * min(1, max_norm / (norm + 1e-6))
+ *   Squares are summed in fp64 in a fixed order (deterministic); *norm is fp32 device.  Where
+ *   the norm is not finite (a gradient holds an infinity or NaN) the gradients are passed on
+ *   unscaled, and the caller decides by *norm.  max_norm = INFINITY takes the norm alone (with
+ *   dst = src nothing is written).
+ *   grads: HOST array of `count` entries, read during the call; src / dst device, aligned to
+ *   their element, dtype SVCONV_F32 or SVCONV_BF16.  dst = src clips in place; any other
+ *   overlap is not allowed.
+ *   workspace >= svconv_clip_grads_workspace_size(grads, count) bytes, 16-byte aligned.
+ *   Limits: count >= 0, numel >= 0; max_norm >= 0 (not NaN).
+ */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  int dtype;
+} svconv_grad;
+SVCONV_API int svconv_clip_grads(const svconv_grad* grads, int count, float max_norm, float* norm, void* workspace,
+                                 size_t ws_bytes, void* stream);
+SVCONV_API size_t svconv_clip_grads_workspace_size(const svconv_grad* grads, int count);
+
+/*
  * The library's own device error word (per device): kernels without a caller
  * status pointer (fwd, bwd_data, bwd_weight) OR SVCONV_STATUS_TIMEOUT and
  * SVCONV_STATUS_BAD_INDEX into it.  Reading it synchronizes the current device,

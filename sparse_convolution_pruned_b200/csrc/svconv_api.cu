@@ -54,7 +54,7 @@ int sm_count() {
   return device_info(d) ? g_sm_count[d] : 1;
 }
 
-static int check_device() {
+int check_device() {
   const int d = current_device();
   if (!device_info(d)) return SVCONV_ERR_CUDA;
   if (g_major[d] != 10) return SVCONV_ERR_DEVICE;

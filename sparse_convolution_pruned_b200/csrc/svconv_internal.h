@@ -12,6 +12,7 @@ namespace svc {
 // The library's per-device error word (defined in svconv_api.cu).
 int* device_error_word();
 int sm_count();
+int check_device();  // SVCONV_OK, or why the current device cannot run the library's kernels
 
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s for any single bounded wait
 

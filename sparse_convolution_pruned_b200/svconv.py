@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -23,10 +23,33 @@ OK = 0
 STATUS_BAD_COORD, STATUS_DUPLICATE, STATUS_BAD_FRAME, STATUS_BAD_OFFSETS = 1, 2, 4, 8
 STATUS_TIMEOUT, STATUS_BAD_INDEX, STATUS_CHUNK_OVERFLOW = 16, 32, 64
 
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsvconv.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "svconv.h")
 _lib = None
+
+
+class CrossAttnDesc(ctypes.Structure):
+    """svconv_cross_attn_desc"""
+    _fields_ = [("nq", ctypes.c_int), ("nkv", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("G", ctypes.c_int), ("q_off", ctypes.c_void_p), ("kv_off", ctypes.c_void_p),
+                ("max_q", ctypes.c_int), ("max_kv", ctypes.c_int), ("kv_keep", ctypes.c_void_p),
+                ("scale", ctypes.c_float)] + \
+        [(f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")]
+
+
+class QkSide(ctypes.Structure):
+    """svconv_qk_side"""
+    _fields_ = [("x", ctypes.c_void_p), ("x_row", ctypes.c_int64), ("n", ctypes.c_int), ("H", ctypes.c_int),
+                ("pos", ctypes.c_void_p), ("w", ctypes.c_void_p), ("y", ctypes.c_void_p), ("dy", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p)]
+
+
+class Grad(ctypes.Structure):
+    """svconv_grad"""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
 
 
 class SvconvError(RuntimeError):
@@ -71,6 +94,24 @@ def lib() -> ctypes.CDLL:
         L.svconv_adapter_fwd_xattn.restype = I
         L.svconv_adapter_xattn_workspace_size.argtypes = [I, I, I, I, I]
         L.svconv_adapter_xattn_workspace_size.restype = Z
+        L.svconv_cross_attn_fwd.argtypes = [P, P, P, P, P, P, P, Z, P, P]
+        L.svconv_cross_attn_fwd.restype = I
+        L.svconv_cross_attn_fwd_workspace_size.argtypes = [P]
+        L.svconv_cross_attn_fwd_workspace_size.restype = Z
+        L.svconv_cross_attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, P, Z, P, P]
+        L.svconv_cross_attn_bwd.restype = I
+        L.svconv_cross_attn_bwd_workspace_size.argtypes = [P]
+        L.svconv_cross_attn_bwd_workspace_size.restype = Z
+        L.svconv_qk_norm_rope_fwd.argtypes = [I, I, I, I, P, I, P, ctypes.c_float, P, P, P]
+        L.svconv_qk_norm_rope_fwd.restype = I
+        L.svconv_qk_norm_rope_bwd.argtypes = [I, I, I, I, P, I, P, ctypes.c_float, P, P, P, Z, P]
+        L.svconv_qk_norm_rope_bwd.restype = I
+        L.svconv_qk_norm_rope_bwd_workspace_size.argtypes = [I]
+        L.svconv_qk_norm_rope_bwd_workspace_size.restype = Z
+        L.svconv_clip_grads.argtypes = [P, I, ctypes.c_float, P, P, Z, P]
+        L.svconv_clip_grads.restype = I
+        L.svconv_clip_grads_workspace_size.argtypes = [P, I]
+        L.svconv_clip_grads_workspace_size.restype = Z
         L.svconv_read_error_word.argtypes = [P]
         L.svconv_selftest_timeout.argtypes = [P, I, P]
         L.svconv_status_str.argtypes = [I]
@@ -352,6 +393,237 @@ def svconv_adapter_fwd_xattn(X: torch.Tensor, nbr: torch.Tensor, frame_off: torc
                                         _stream(X, stream))
     _check("svconv_adapter_fwd_xattn", rc)
     return X, aux_out
+
+
+def _heads_first(name: str, t: torch.Tensor):
+    """[n, H, d] bf16 with contiguous channels; rows and heads may be strided (a slice of a fused projection)."""
+    if not t.is_cuda:
+        raise ValueError("svconv operates on CUDA tensors only")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: bf16 is needed, got {t.dtype}")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name}: [rows, heads, channels] with contiguous channels is needed")
+
+
+def _like(name: str, t: torch.Tensor, shape, dtype, dev):
+    _cuda(t)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name}: {tuple(shape)} {dtype} on {dev} is needed, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _ensure(name: str, t: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _like(name, t, shape, dtype, dev)
+    return t
+
+
+def _on(dev: torch.device):
+    """Makes the tensors' device current for a call (launches and device queries go to the current device)."""
+    return torch.cuda.device(dev)
+
+
+def _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep) -> CrossAttnDesc:
+    for name, t in (("Q", Q), ("K", K), ("V", V)):
+        _heads_first(name, t)
+        if t.device != Q.device:
+            raise ValueError(f"{name} is on {t.device}, Q on {Q.device}")
+    nq, Hq, d = Q.shape
+    nkv, Hkv, _ = K.shape
+    if K.shape[2] != d or V.shape != K.shape:
+        raise ValueError(f"Q {tuple(Q.shape)}, K {tuple(K.shape)} and V {tuple(V.shape)} do not fit together")
+    G = q_off.numel() - 1
+    for name, t in (("q_off", q_off), ("kv_off", kv_off)):
+        _like(name, t, (max(G, 0) + 1,), torch.int32, Q.device)
+    if kv_keep is not None:
+        if kv_keep.dtype not in (torch.uint8, torch.bool):
+            raise TypeError(f"kv_keep: uint8 or bool is needed, got {kv_keep.dtype}")
+        _like("kv_keep", kv_keep, (nkv,), kv_keep.dtype, Q.device)
+    return CrossAttnDesc(nq, nkv, Hq, Hkv, d, G, q_off.data_ptr(), kv_off.data_ptr(), int(max_q), int(max_kv),
+                         kv_keep.data_ptr() if kv_keep is not None else None,
+                         float(scale) if scale is not None else d ** -0.5, Q.stride(0), Q.stride(1), K.stride(0),
+                         K.stride(1), V.stride(0), V.stride(1))
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, dev) -> Tuple[Optional[torch.Tensor], int]:
+    if ws is None:
+        if not need:
+            return None, 0
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _cuda(ws)
+    if ws.device != dev:
+        raise ValueError(f"workspace is on {ws.device}, the inputs on {dev}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def svconv_cross_attn_fwd_workspace_size(desc: CrossAttnDesc) -> int:
+    return int(lib().svconv_cross_attn_fwd_workspace_size(ctypes.byref(desc)))
+
+
+def svconv_cross_attn_bwd_workspace_size(desc: CrossAttnDesc) -> int:
+    return int(lib().svconv_cross_attn_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def svconv_cross_attn_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_off: torch.Tensor,
+                          kv_off: torch.Tensor, *, max_q: int, max_kv: int, scale: Optional[float] = None,
+                          kv_keep: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Q [nq, Hq, d] attending over K, V [nkv, Hkv, d] of its group -> (O [nq, Hq, d] bf16, lse [nq, Hq] fp32).
+
+    scale defaults to 1 / sqrt(d); kv_keep [nkv] (uint8 or bool) leaves keys out.  Rows of no group
+    are not written."""
+    desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
+    dev = Q.device
+    _cuda(status)
+    out = _ensure("out", out, Q.shape, torch.bfloat16, dev)
+    lse = _ensure("lse", lse, Q.shape[:2], torch.float32, dev)
+    with _on(dev):
+        workspace, ws_bytes = _workspace(workspace, svconv_cross_attn_fwd_workspace_size(desc), dev)
+        rc = lib().svconv_cross_attn_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(out), _ptr(lse),
+                                         _ptr(workspace), ws_bytes, _ptr(status), _stream(Q, stream))
+    _check("svconv_cross_attn_fwd", rc)
+    return out, lse
+
+
+def svconv_cross_attn_bwd(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+                          lse: torch.Tensor, q_off: torch.Tensor, kv_off: torch.Tensor, *, max_q: int, max_kv: int,
+                          scale: Optional[float] = None, kv_keep: Optional[torch.Tensor] = None,
+                          dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+                          dV: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None, stream=None):
+    """(dQ, dK, dV) of svconv_cross_attn_fwd from dO and the forward's O and lse; contiguous bf16."""
+    desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
+    dev = Q.device
+    _cuda(status)
+    _like("dO", dO, Q.shape, torch.bfloat16, dev)
+    _like("O", O, Q.shape, torch.bfloat16, dev)
+    _like("lse", lse, Q.shape[:2], torch.float32, dev)
+    dQ = _ensure("dQ", dQ, Q.shape, torch.bfloat16, dev)
+    dK = _ensure("dK", dK, K.shape, torch.bfloat16, dev)
+    dV = _ensure("dV", dV, V.shape, torch.bfloat16, dev)
+    with _on(dev):
+        workspace, ws_bytes = _workspace(workspace, svconv_cross_attn_bwd_workspace_size(desc), dev)
+        rc = lib().svconv_cross_attn_bwd(ctypes.byref(desc), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
+                                         _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace), ws_bytes, _ptr(status),
+                                         _stream(Q, stream))
+    _check("svconv_cross_attn_bwd", rc)
+    return dQ, dK, dV
+
+
+_ROPE_LAYOUTS = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED, ROPE_HALF: ROPE_HALF,
+                 ROPE_INTERLEAVED: ROPE_INTERLEAVED}
+
+
+def _qk_common(Q, K, pq, pk, freq, layout, axis_pairs, wq, wk):
+    """Checked sides, the shared arguments of both directions."""
+    dev, dt, d = Q.device, _dtype_code(Q), Q.shape[-1]
+    if dt == E4M3:
+        raise TypeError("svconv_qk_norm_rope takes fp32 or bf16")
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r}: 'half' or 'interleaved'")
+    _like("freq", freq, (freq.numel(),), torch.float64, dev)
+    axes = pq.shape[1] if pq.dim() == 2 else 1
+    split = [freq.numel()] if axis_pairs is None else [int(a) for a in axis_pairs]
+    if len(split) != axes or sum(split) != freq.numel():
+        raise ValueError(f"axis_pairs {split}: {axes} counts that add up to {freq.numel()} frequencies are needed")
+    sides = []
+    for name, x, pos, w in (("Q", Q, pq, wq), ("K", K, pk, wk)):
+        if not x.is_cuda:
+            raise ValueError("svconv operates on CUDA tensors only")
+        if x.dim() != 3 or x.shape[2] != d or x.dtype != Q.dtype or x.device != dev:
+            raise ValueError(f"{name}: [rows, heads, {d}] {Q.dtype} on {dev} is needed")
+        n, H, _ = x.shape
+        if x.numel() and ((d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d)):
+            raise ValueError(f"{name}: contiguous heads are needed (rows may be strided)")
+        _like(f"positions of {name}", pos, (n, axes) if pos.dim() == 2 else (n,), torch.int32, dev)
+        if (pos.shape[1] if pos.dim() == 2 else 1) != axes:
+            raise ValueError("the positions of Q and K have different numbers of axes")
+        if w is not None:
+            _like(f"weight of {name}", w, (d,), torch.float32, dev)
+        sides.append(QkSide(x.data_ptr(), x.stride(0) if n > 1 else H * d, n, H, pos.data_ptr(),
+                            w.data_ptr() if w is not None else None, None, None, None, None))
+    split_c = (ctypes.c_int32 * 3)(*split)
+    return dev, sides, (dt, d, 2 * freq.numel(), _ROPE_LAYOUTS[layout], _ptr(freq), axes, split_c)
+
+
+def svconv_qk_norm_rope_fwd(Q: torch.Tensor, K: torch.Tensor, pos_q: torch.Tensor, pos_k: torch.Tensor,
+                            freq: torch.Tensor, *, wq: Optional[torch.Tensor] = None,
+                            wk: Optional[torch.Tensor] = None, eps: float = 1e-6, layout="half", axis_pairs=None,
+                            Yq: Optional[torch.Tensor] = None, Yk: Optional[torch.Tensor] = None, stream=None):
+    """Per-head RMS norm of Q [nq, Hq, d] and K [nk, Hkv, d] (fp32 or bf16) with their tokens' rotary positions.
+
+    pos_* int32 [n] or [n, axes] (the (t, y, x) coords table serves as it is), freq fp64 [rot / 2] radians
+    per unit of position (the first 2 * len(freq) channels are rotated), axis_pairs the number of pairs that
+    follow each axis.  Yq / Yk may be Q / K themselves when those are contiguous."""
+    dev, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
+    Yq = _ensure("Yq", Yq, Q.shape, Q.dtype, dev)
+    Yk = _ensure("Yk", Yk, K.shape, K.dtype, dev)
+    sq.y, sk.y = Yq.data_ptr(), Yk.data_ptr()
+    with _on(dev):
+        rc = lib().svconv_qk_norm_rope_fwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _stream(Q, stream))
+    _check("svconv_qk_norm_rope_fwd", rc)
+    return Yq, Yk
+
+
+def svconv_qk_norm_rope_bwd_workspace_size(d: int) -> int:
+    return int(lib().svconv_qk_norm_rope_bwd_workspace_size(int(d)))
+
+
+def svconv_qk_norm_rope_bwd(dYq: torch.Tensor, dYk: torch.Tensor, Q: torch.Tensor, K: torch.Tensor,
+                            pos_q: torch.Tensor, pos_k: torch.Tensor, freq: torch.Tensor, *,
+                            wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                            layout="half", axis_pairs=None, dQ: Optional[torch.Tensor] = None,
+                            dK: Optional[torch.Tensor] = None, dwq: Optional[torch.Tensor] = None,
+                            dwk: Optional[torch.Tensor] = None, want_dw: bool = True,
+                            workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dQ, dK, dwq, dwk) of svconv_qk_norm_rope_fwd (dwq, dwk fp32 [d], None unless want_dw)."""
+    dev, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
+    d = Q.shape[2]
+    _like("dYq", dYq, Q.shape, Q.dtype, dev)
+    _like("dYk", dYk, K.shape, K.dtype, dev)
+    dQ = _ensure("dQ", dQ, Q.shape, Q.dtype, dev)
+    dK = _ensure("dK", dK, K.shape, K.dtype, dev)
+    if want_dw:
+        dwq = _ensure("dwq", dwq, (d,), torch.float32, dev)
+        dwk = _ensure("dwk", dwk, (d,), torch.float32, dev)
+    for s, dy, dx, dw in ((sq, dYq, dQ, dwq), (sk, dYk, dK, dwk)):
+        s.dy, s.dx, s.dw = dy.data_ptr(), dx.data_ptr(), dw.data_ptr() if dw is not None else None
+    with _on(dev):
+        workspace, ws_bytes = _workspace(workspace, svconv_qk_norm_rope_bwd_workspace_size(d), dev)
+        rc = lib().svconv_qk_norm_rope_bwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _ptr(workspace),
+                                           ws_bytes, _stream(Q, stream))
+    _check("svconv_qk_norm_rope_bwd", rc)
+    return dQ, dK, dwq, dwk
+
+
+def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
+                      norm: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Scale the gradients (fp32 or bf16, contiguous, one device) by min(1, max_norm / (norm + 1e-6)), in place
+    or into `out`; returns their global norm (fp32 scalar tensor).  max_norm = inf takes the norm alone."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+    if not grads and norm is None:
+        raise ValueError("no gradients and no norm tensor: the device is unknown")
+    dev = grads[0].device if grads else norm.device
+    table = (Grad * max(len(grads), 1))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        _cuda(g, o)
+        if g.device != dev or o.device != dev or o.dtype != g.dtype or o.shape != g.shape:
+            raise ValueError(f"gradient {i}: one device, and outputs of the gradients' shapes and types are needed")
+        e = table[i]
+        e.src, e.dst, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)
+    norm = _ensure("norm", norm, (), torch.float32, dev)
+    with _on(dev):
+        need = int(lib().svconv_clip_grads_workspace_size(table, len(grads)))
+        workspace, ws_bytes = _workspace(workspace, max(need, 16), dev)
+        rc = lib().svconv_clip_grads(table, len(grads), float(max_norm), _ptr(norm), _ptr(workspace), ws_bytes,
+                                     _stream(norm, stream))
+    _check("svconv_clip_grads", rc)
+    return norm
 
 
 def svconv_read_error_word() -> int:

@@ -1,0 +1,310 @@
+"""svconv_cross_attn_fwd / _bwd against the formulas in 64 bits.
+
+Bounds, element by element.  A bf16 rounding is off by at most u = 2^-8 of the value.  Forward:
+the weights P are rounded once as matrix operands and O once at the end, so |err| <= u (sum_j P |V|
++ |O|).  Backward: P and dS are rounded once each, D = dO . O takes the rounded O (off by at most
+dD = u sum_c |dO| (|O| + sum_j P |V|)), and each gradient is rounded at the end:
+    dV:  u (P^T |dO| + |dV|)
+    dQ:  u (scale |dS| |K| + |dQ|) + scale (P dD) |K|,   dK the same with |Q| and the transposes.
+5% on top covers the products of these terms and the fp32 sums; lse is an fp32 sum of fp32 scores,
+whose d products each round by 2^-24 of their magnitude.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U = torch.finfo(torch.bfloat16).eps / 2
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_convolution_pruned_b200 import build, svconv
+    build.build()
+    assert svconv.svconv_read_error_word() == 0
+    return svconv
+
+
+def offsets(lens, start=0):
+    return torch.tensor(np.concatenate([[start], start + np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def make(seed, q_lens, kv_lens, Hq, Hkv, d, keep=1.0, gap=0, fused=False, scale=1.0):
+    """Inputs with `gap` rows of no group before the first and after the last one."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    nq, nk = sum(q_lens) + 2 * gap, sum(kv_lens) + 2 * gap
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = {"Q": (scale * rnd(nq, Hq, d)).bfloat16()}
+    if fused:  # K and V as slices of one projection of [K | V | something else]
+        kv = rnd(nk, 2 * Hkv + 1, d).bfloat16()
+        x["K"], x["V"] = kv[:, :Hkv], kv[:, Hkv:2 * Hkv]
+    else:
+        x["K"], x["V"] = rnd(nk, Hkv, d).bfloat16(), rnd(nk, Hkv, d).bfloat16()
+    x["dO"] = rnd(nq, Hq, d).bfloat16()
+    x["q_off"], x["kv_off"] = offsets(q_lens, gap), offsets(kv_lens, gap)
+    x["keep"] = (torch.rand((nk,), generator=gen, device="cuda") < keep).to(torch.uint8) if keep < 1 else None
+    x["max_q"], x["max_kv"] = max(q_lens), max(kv_lens)
+    return x
+
+
+def reference(x, scale, O_used=None):
+    """O, lse, dQ, dK, dV in fp64 with their bounds, group by group and head by head."""
+    Q, K, V, dO = (x[k].double() for k in ("Q", "K", "V", "dO"))
+    nq, Hq, d = Q.shape
+    r = Hq // K.shape[1]
+    z = lambda t: torch.zeros_like(t)
+    out = {k: z(t) for k, t in (("O", Q), ("dQ", Q), ("dK", K), ("dV", V))}
+    tol = {k: z(t) for k, t in out.items()}
+    out["lse"] = torch.full((nq, Hq), -math.inf, dtype=torch.float64, device="cuda")
+    tol["lse"] = torch.zeros((nq, Hq), dtype=torch.float64, device="cuda")
+    qo, ko = x["q_off"].tolist(), x["kv_off"].tolist()
+    for g in range(len(qo) - 1):
+        a, b = torch.arange(qo[g], qo[g + 1], device="cuda"), torch.arange(ko[g], ko[g + 1], device="cuda")
+        if x["keep"] is not None:
+            b = b[x["keep"][b] != 0]
+        if len(a) == 0 or len(b) == 0:
+            continue
+        for h in range(Hq):
+            q, k, v, do = Q[a, h], K[b, h // r], V[b, h // r], dO[a, h]
+            s = scale * q @ k.T
+            lse = torch.logsumexp(s, 1, keepdim=True)
+            P = torch.exp(s - lse)
+            O, A = P @ v, P @ v.abs()
+            out["O"][a, h], out["lse"][a, h] = O, lse[:, 0]
+            tol["O"][a, h] = U * (A + O.abs())
+            tol["lse"][a, h] = 2.0 ** -20 * (1 + lse[:, 0].abs()) + 2.0 ** -24 * (d + 8) * abs(scale) * (q.abs() @ k.abs().T).amax(1)
+            dS = P * (do @ v.T - (do * O).sum(1, keepdim=True))
+            slop = P * (U * (do.abs() * (O.abs() + A)).sum(1, keepdim=True))
+            dq = scale * dS @ k
+            out["dQ"][a, h] = dq
+            tol["dQ"][a, h] = abs(scale) * (U * dS.abs() + slop) @ k.abs() + U * dq.abs()
+            out["dK"][b, h // r] += scale * dS.T @ q
+            tol["dK"][b, h // r] += abs(scale) * (U * dS.abs() + slop).T @ q.abs()
+            out["dV"][b, h // r] += P.T @ do
+            tol["dV"][b, h // r] += U * P.T @ do.abs()
+    for k in ("dK", "dV"):
+        tol[k] += U * out[k].abs()
+    return out, tol
+
+
+def close(got, ref, tol, what):
+    got = got.double()
+    fin = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got), fin), f"{what}: finite in other places"
+    assert torch.equal(got[~fin], ref[~fin]), what
+    over = (got - ref).abs()[fin] - 1.05 * tol[fin] - 1e-30
+    assert over.numel() == 0 or float(over.max()) <= 0, f"{what}: {float(over.max()):.3e} over its bound"
+
+
+def run_both(sv, x, scale=None, backward=True, **kw):
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dict(max_q=x["max_q"], max_kv=x["max_kv"], kv_keep=x["keep"], scale=scale, status=st)
+    args.update(kw)
+    sentinel = 7.0
+    O = torch.full_like(x["Q"], sentinel)
+    lse = torch.full(x["Q"].shape[:2], sentinel, device="cuda")
+    sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], out=O, lse=lse, **args)
+    got = {"O": O, "lse": lse}
+    if backward:
+        dQ = torch.full_like(x["Q"], sentinel)
+        dK, dV = (torch.full(x["K"].shape, sentinel, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], O, lse, x["q_off"], x["kv_off"], dQ=dQ, dK=dK, dV=dV, **args)
+        got.update(dQ=dQ, dK=dK, dV=dV)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and sv.svconv_read_error_word() == 0
+    return got
+
+
+def check(x, got, scale, what):
+    ref, tol = reference(x, scale)
+    spans = {"O": "q_off", "lse": "q_off", "dQ": "q_off", "dK": "kv_off", "dV": "kv_off"}
+    for k, t in got.items():
+        lo, hi = int(x[spans[k]][0]), int(x[spans[k]][-1])
+        close(t[lo:hi], ref[k][lo:hi], tol[k][lo:hi], f"{what} {k}")
+        for part in (t[:lo], t[hi:]):  # rows of no group are left as they were
+            assert (part == 7.0).all(), f"{what}: {k} written outside the groups"
+
+
+CASES = [
+    # q lengths, kv lengths, Hq, Hkv, d, keep, gap, fused
+    ((1,), (1,), 1, 1, 64, 1.0, 0, False),
+    ((1,), (128,), 4, 4, 64, 1.0, 0, False),
+    ((1, 1, 1), (129, 0, 257), 2, 1, 128, 1.0, 3, False),
+    ((127, 128, 129), (127, 128, 129), 2, 2, 64, 1.0, 0, False),
+    ((300, 0, 5, 64), (7, 40, 0, 500), 4, 2, 128, 1.0, 2, False),
+    ((257,), (1000,), 3, 1, 64, 0.7, 0, False),
+    ((33, 260), (129, 65), 5, 1, 96, 0.9, 1, True),
+    ((65, 1), (3, 700), 6, 2, 40, 1.0, 0, True),
+    ((40,), (90,), 2, 2, 8, 1.0, 5, False),
+    ((90, 12), (17, 150), 2, 2, 24, 0.5, 0, False),
+    ((70, 130), (300, 2), 4, 4, 80, 1.0, 0, True),
+    ((520,), (640,), 1, 1, 16, 1.0, 0, False),
+    ((3,), (5000,), 7, 7, 32, 0.95, 0, False),
+    ((2, 30), (6000, 4100), 8, 1, 128, 1.0, 0, False),
+    ((1100,), (30,), 2, 2, 72, 1.0, 0, False),
+    ((385, 700), (513, 900), 2, 1, 128, 0.8, 0, False),
+    ((20,), (60,), 128, 1, 64, 1.0, 0, False),
+    ((1,), (20000,), 4, 4, 64, 1.0, 0, False),
+    ((2300,), (100,), 4, 4, 64, 1.0, 0, False),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_against_the_formulas(sv, i):
+    q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused = CASES[i]
+    x = make(100 + i, q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused)
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, CASES[i])
+    again = run_both(sv, x)
+    for k in got:
+        assert torch.equal(got[k], again[k]), f"{k} differs between two calls"
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_scales(sv, scale):
+    x = make(7, (140, 3), (260, 31), 2, 2, 64)
+    check(x, run_both(sv, x, scale=scale), scale, f"scale {scale}")
+
+
+def test_large_scores_saturate_without_overflow(sv):
+    """Scores of several hundred: the softmax collapses onto single keys."""
+    x = make(8, (130,), (400,), 2, 2, 64, scale=60.0)
+    check(x, run_both(sv, x), 64 ** -0.5, "saturated")
+
+
+def test_rising_scores_move_the_running_maximum(sv):
+    """Keys whose scores rise along the sequence: every key tile moves the maximum."""
+    x = make(9, (150, 2), (1500, 2100), 2, 2, 64)
+    for g in range(2):
+        lo, hi = int(x["kv_off"][g]), int(x["kv_off"][g + 1])
+        ramp = torch.linspace(-30.0, 30.0, hi - lo, device="cuda")
+        x["K"][lo:hi, :, 0] = ramp[:, None].bfloat16()
+    x["Q"][:, :, 0] = 8.0
+    check(x, run_both(sv, x), 64 ** -0.5, "rising")
+
+
+@pytest.mark.parametrize("d,lens", [(64, ((200, 40), (300, 150))), (128, ((3, 2), (900, 400)))])
+def test_masked_and_foreign_rows_may_hold_anything(sv, d, lens):
+    """NaN and infinities in dropped keys, and in rows of other groups and of no group."""
+    x = make(11, lens[0], lens[1], 2, 2, d, keep=0.6, gap=9)
+    ko, qo = x["kv_off"].tolist(), x["q_off"].tolist()
+    x["keep"][ko[0] + 128:ko[0] + 256] = 0  # a whole tile of keys dropped
+    clean = run_both(sv, x)
+    check(x, clean, d ** -0.5, "clean")
+    bad = torch.tensor([math.nan, math.inf, -math.inf], device="cuda").bfloat16()
+    drop = (x["keep"] == 0).nonzero()[:, 0]
+    for t in (x["K"], x["V"]):
+        t[drop] = bad[torch.arange(len(drop), device="cuda") % 3][:, None, None]
+        t[:ko[0]] = math.nan
+        t[ko[-1]:] = math.inf
+    for t in (x["Q"], x["dO"]):
+        t[:qo[0]] = math.nan
+        t[qo[-1]:] = math.inf
+    dirty = run_both(sv, x)
+    for k in clean:
+        assert torch.equal(clean[k], dirty[k]), k
+    # group 1 poisoned as a whole: group 0 keeps its values
+    x["K"][ko[1]:], x["V"][ko[1]:], x["Q"][qo[1]:], x["dO"][qo[1]:] = math.nan, math.nan, math.nan, math.nan
+    dirty = run_both(sv, x)
+    for k, off in (("O", qo), ("lse", qo), ("dQ", qo), ("dK", ko), ("dV", ko)):
+        assert torch.equal(clean[k][off[0]:off[1]], dirty[k][off[0]:off[1]]), k
+
+
+def test_rows_without_any_key(sv):
+    """A group whose mask drops every key, and one without keys: O = 0, lse = -inf, gradients 0."""
+    x = make(12, (40, 30, 20), (200, 0, 10), 2, 1, 64, keep=0.5)
+    x["keep"][:200] = 0
+    got = run_both(sv, x)
+    check(x, got, 0.125, "no keys")
+    assert (got["O"][:70] == 0).all() and torch.isinf(got["lse"][:70]).all() and (got["dQ"][:70] == 0).all()
+    assert (got["dK"][:200] == 0).all() and (got["dV"][:200] == 0).all()
+
+
+def test_keys_without_queries_get_zero_gradients(sv):
+    x = make(13, (0, 4), (300, 20), 2, 2, 64)
+    got = run_both(sv, x)
+    assert (got["dK"][:300] == 0).all() and (got["dV"][:300] == 0).all()
+    check(x, got, 0.125, "no queries")
+
+
+def test_gradients_against_differences(sv):
+    """The backward pass against central differences of the fp64 forward formula."""
+    x = make(14, (9, 5), (21, 12), 4, 2, 16)
+    got = run_both(sv, x)
+    ref, tol = reference(x, 0.25)
+    f = lambda y: float((reference(y, 0.25)[0]["O"] * x["dO"].double()).sum())
+    rng = np.random.default_rng(0)
+    for name, grad in (("Q", "dQ"), ("K", "dK"), ("V", "dV")):
+        step = torch.from_numpy(rng.standard_normal(tuple(x[name].shape))).cuda()
+        eps = 1e-5
+        up, dn = dict(x), dict(x)
+        up[name], dn[name] = x[name].double() + eps * step, x[name].double() - eps * step
+        slope = (f(up) - f(dn)) / (2 * eps)
+        assert abs(slope - float((ref[grad] * step).sum())) <= 1e-6 * (1 + abs(slope))
+        assert abs(slope - float((got[grad].double() * step).sum())) <= float((1.05 * tol[grad] * step.abs()).sum()) + 1e-5
+
+
+def test_larger_groups_than_the_bound_are_flagged(sv):
+    x = make(15, (40, 8), (300, 20), 2, 2, 64)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    full, _ = sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], max_q=40, max_kv=300)
+    O = torch.full_like(x["Q"], 7.0)
+    sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], max_q=16, max_kv=300, status=st, out=O)
+    torch.cuda.synchronize()
+    assert int(st.item()) == sv.STATUS_CHUNK_OVERFLOW
+    assert torch.equal(O[:16], full[:16]) and (O[16:40] == 7.0).all() and torch.equal(O[40:], full[40:])
+
+
+def test_bad_offsets_are_flagged_and_their_groups_skipped(sv):
+    x = make(16, (40, 8), (300, 20), 2, 2, 64)
+    want = run_both(sv, x)
+    for bad in ([0, 300, 100000], [0, 300, 200], [-4, 300, 320]):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        g = 0 if bad[0] < 0 else 1
+        O = torch.full_like(x["Q"], 7.0)
+        lse = torch.full(x["Q"].shape[:2], 7.0, device="cuda")
+        kw = dict(max_q=40, max_kv=300, status=st)
+        sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], off, out=O, lse=lse, **kw)
+        dQ, dK, dV = torch.full_like(x["Q"], 7.0), torch.full_like(x["K"], 7.0), torch.full_like(x["V"], 7.0)
+        sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], want["O"], want["lse"], x["q_off"], off, dQ=dQ,
+                                 dK=dK, dV=dV, **kw)
+        torch.cuda.synchronize()
+        assert int(st.item()) == sv.STATUS_BAD_OFFSETS, bad
+        good = slice(0, 40) if g == 1 else slice(40, 48)
+        assert torch.equal(O[good], want["O"][good]) and torch.equal(dQ[good], want["dQ"][good])
+        skipped = slice(40, 48) if g == 1 else slice(0, 40)
+        assert (O[skipped] == 7.0).all() and (dQ[skipped] == 7.0).all() and (lse[skipped] == 7.0).all()
+    assert sv.svconv_read_error_word() == 0
+
+
+def test_streams_and_captured_graphs(sv):
+    """A side stream, and two captured graphs (a workspace each) replayed on two streams."""
+    xs = [make(20 + i, (33, 200), (2500, 700), 4, 2, 64) for i in range(2)]
+    want = [run_both(sv, x) for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            run_both(sv, x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            O, lse = sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], max_q=200, max_kv=2500)
+            d = sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], O, lse, x["q_off"], x["kv_off"], max_q=200,
+                                         max_kv=2500)
+        graphs.append((g, s))
+        outs.append(dict(zip(("O", "lse", "dQ", "dK", "dV"), (O, lse) + d)))
+    for _ in range(3):
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for k in w:
+            assert torch.equal(o[k], w[k]), k
+    assert sv.svconv_read_error_word() == 0
