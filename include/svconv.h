@@ -306,7 +306,7 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *   workspace  >= svconv_cross_attn_fwd_workspace_size(desc) bytes, 16-byte aligned (may be
  *              NULL if that is 0), no initial contents required.  Calls that overlap on the GPU
  *              (captured graphs included) need a workspace each.
- *   Limits: d a multiple of 8, 8 <= d <= 128; Hq a multiple of Hkv, Hq / Hkv <= 128;
+ *   Limits: d a multiple of 8, 8 <= d <= 128; Hq a multiple of Hkv, Hq / Hkv <= 64;
  *   scale finite.  Deterministic: bitwise identical results for identical calls.
  *
  * svconv_cross_attn_bwd: with dO [nq][Hq][d] bf16 and O, lse of the forward call,

@@ -1,8 +1,6 @@
 // Cross-attention of packed groups, forward and backward: every query row attends over the kept
 // keys of its group (see svconv_cross_attn_fwd in svconv.h for the definition).
-//
-// CUDA-core form: one warp per (query row, head) forward and for dQ, one warp per (key row, key
-// head) for dK and dV.  Scores are in base 2 (scale * log2 e folded into one factor).
+// Scores are in base 2: scale * log2(e) is one factor, and every exponential is one ex2.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -18,21 +16,6 @@ namespace {
 constexpr int kMaxD = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 8;
-
-struct AttnParams {
-  const __nv_bfloat16 *Q, *K, *V, *O, *dO;
-  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
-  int nq, nkv, Hq, Hkv, r, d, G;
-  const int32_t *q_off, *kv_off;
-  int max_q, max_kv;
-  const uint8_t* keep;
-  float scale;
-  __nv_bfloat16 *dQ, *dK, *dV;
-  const float* lse;
-  float* D;
-  int* status;
-};
 
 // Rows lo .. hi-1 of group g, clipped to the bound; flags for the status word.
 __device__ __forceinline__ int group_range(const int32_t* off, int g, int n, int bound, int& lo, int& hi) {
@@ -47,25 +30,6 @@ __device__ __forceinline__ int group_range(const int32_t* off, int g, int n, int
     return SVCONV_STATUS_CHUNK_OVERFLOW;
   }
   return 0;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-__device__ __forceinline__ float dot_row(const float* a, const __nv_bfloat16* b, int d) {
-  float s = 0.f;
-  for (int c = 0; c < d; c += 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(b + c);
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      s = fmaf(a[c + 2 * i], f.x, s);
-      s = fmaf(a[c + 2 * i + 1], f.y, s);
-    }
-  }
-  return s;
 }
 
 // ============================================================================ tensor-core building blocks
@@ -124,14 +88,15 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 
 // Zero the rows of a tile that must not reach a product (0 x NaN): bit j of drop[w] is row 32 w + j.
 // One warp; a row is 128 contiguous bytes of each 64-channel block whatever the swizzle.
-__device__ __forceinline__ void scrub_rows(uint32_t tile, int blocks, const uint32_t (&drop)[4]) {
+template <int WORDS>
+__device__ __forceinline__ void scrub_rows(uint32_t tile, int blocks, uint32_t block_bytes, const uint32_t (&drop)[WORDS]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WORDS; ++w) {
     if (drop[w] >> lane & 1u)
       for (int b = 0; b < blocks; ++b)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st_shared_16(tile + b * kBlockBytes + (32 * w + lane) * 128 + ((i + lane) & 7) * 16, 0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) st_shared_16(tile + b * block_bytes + (32 * w + lane) * 128 + ((i + lane) & 7) * 16, 0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -281,7 +246,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             kept_words(p.keep, j0, k1, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = ~w[i];
-            scrub_rows(skv + (n % NS) * Sh::kTileBytes, DB, w);
+            scrub_rows(skv + (n % NS) * Sh::kTileBytes, DB, kBlockBytes, w);
           }
         }
         return true;
@@ -573,101 +538,422 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
   if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) attn_dq_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ float sq[kWarps][kMaxD], sdo[kWarps][kMaxD];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int g = blockIdx.z, h = blockIdx.y;
+// ============================================================================ backward
+// Two passes over the scores, both of one form: a CTA holds a fixed tile of 128 rows (two operands F1,
+// F2) and runs over moving tiles of 64 rows (M1, M2), its two softmax warpgroups taking alternate
+// moving tiles (streams) while both add to the same accumulators in tensor memory.
+//                   fixed F1, F2   moving M1, M2   scores          accumulates
+//   key pass        K, V           Q, dO           S^T, dP^T       dV += P^T dO, dK += dS^T Q
+//   query pass      Q, dO          K, V            S, dP           dQ += dS K
+// With the scores transposed in the key pass, P^T and dS^T are written row by row as A operands in
+// tensor memory, and M1, M2 serve both as K-major operands of the scores and as MN-major operands of the
+// sums: nothing is transposed and nothing passes through shared memory.  No atomics: each output
+// row has one owner, or one per split with the splits added in a fixed order.  That costs 7 products
+// per tile where one pass with atomics on dQ would take 5.
+constexpr int kMove = 64;                  // rows of a moving tile
+constexpr int kMoveBlock = kMove * 128;    // bytes of its 64-channel block
+constexpr int kStatBytes = 544;            // lse and D of 64 rows (8 bytes each) from a 16-byte boundary on
+
+struct BwdParams {
+  CUtensorMap fq, fdo, fk, fv;   // boxes of the fixed tiles
+  CUtensorMap mq, mdo, mk, mv;   // boxes of the moving tiles
+  const int32_t *q_off, *kv_off;
+  const uint8_t* keep;
+  int nq, nkv, max_q, max_kv, Hq, Hkv, r, d;
+  int qblocks, qsplits, kblocks, ksplits;
+  int q_items;                   // CTAs of the query pass (they come first)
+  float c, scale;
+  const float2* stat;            // [Hkv][nq * r]: lse in base 2 (+inf for a row without keys), D
+  __nv_bfloat16 *dQ, *dK, *dV;
+  float *part_q, *part_k, *part_v;  // [splits][rows][d] where a pass is split
+  int* status;
+};
+
+struct BwdBarriers {
+  uint64_t ffull, mfull[8], mempty[8], sfull[2], pfull[2], pdone[2], adone[2], fin;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int DB>
+struct BwdShape {
+  static constexpr int kFixedBytes = DB * kBlockBytes, kMoveBytes = DB * kMoveBlock;
+  static constexpr int kStages = DB == 1 ? 8 : 4;
+  static constexpr int kStageBytes = 2 * kMoveBytes;
+  static constexpr size_t kSmem = 1024 + 2 * kFixedBytes + kStages * (size_t)(kStageBytes + kStatBytes) + sizeof(BwdBarriers);
+};
+
+// Tensor-memory columns.  P and dS have columns of their own except in the key pass at 128
+// channels, where the accumulators leave room for the scores alone and P, dS take their place.
+template <int DB, bool KEYS>
+struct BwdTmem {
+  static constexpr bool kShared = DB == 2 && KEYS;
+  static constexpr int kStride = DB == 1 ? 192 : KEYS ? 128 : 160;
+  static constexpr int S(int s) { return s * kStride; }
+  static constexpr int dP(int s) { return s * kStride + 64; }
+  static constexpr int P(int s) { return DB == 1 ? s * kStride + 128 : s * kStride; }
+  static constexpr int dS(int s) { return DB == 1 ? s * kStride + 160 : KEYS ? s * kStride + 64 : s * kStride + 128; }
+  static constexpr int kAcc1 = DB == 1 ? 384 : 256;   // dV
+  static constexpr int kAcc2 = DB == 1 ? 448 : 384;   // dK or dQ
+};
+
+template <int DB, bool KEYS>
+__device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t base, BwdBarriers* bar, const uint8_t* stats) {
+  using Sh = BwdShape<DB>;
+  using Tm = BwdTmem<DB, KEYS>;
+  constexpr int NS = Sh::kStages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bar->abort_flag;
+  int* err = p.status;
+  const uint32_t sf = base, sm = base + 2 * Sh::kFixedBytes;
+  const uint32_t sstat = sm + NS * Sh::kStageBytes;
+  const uint32_t tmem = bar->tmem;
+
+  const int blocks = KEYS ? p.kblocks : p.qblocks, splits = KEYS ? p.ksplits : p.qsplits;
+  const int block = item % blocks;
+  item /= blocks;
+  const int split = item % splits;
+  item /= splits;
+  const int hk = item % p.Hkv, g = item / p.Hkv;
   int q0, q1, k0, k1;
   const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
-  if (flags && threadIdx.x == 0 && blockIdx.x == 0 && h == 0) atomicOr(p.status, flags);
-  if (flags & SVCONV_STATUS_BAD_OFFSETS) return;
-  const int row = q0 + blockIdx.x * kWarps + w;
-  if (row >= q1) return;
-  const int64_t at = ((int64_t)row * p.Hq + h);
-  float D = 0.f;
-  for (int c = lane; c < p.d; c += 32) {
-    sq[w][c] = __bfloat162float(p.Q[row * p.q_row + h * p.q_head + c]) * (p.scale * kLog2e);
-    const float go = __bfloat162float(p.dO[at * p.d + c]);
-    sdo[w][c] = go;
-    D = fmaf(go, __bfloat162float(p.O[at * p.d + c]), D);
-  }
-  D = warp_sum(D);
-  __syncwarp();
-  if (lane == 0) p.D[at] = D;
-  const int hk = h / p.r;
-  const float lse2 = p.lse[at] * kLog2e;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int j0 = k0; j0 < k1; j0 += 32) {
-    const int j = j0 + lane;
-    const bool ok = j < k1 && (!p.keep || p.keep[j]);
-    float ds = 0.f;
-    if (ok) {
-      const float s = dot_row(sq[w], p.K + j * p.k_row + hk * p.k_head, p.d);
-      ds = exp2f(s - lse2) * (dot_row(sdo[w], p.V + j * p.v_row + hk * p.v_head, p.d) - D);
-    }
-    const unsigned kept = __ballot_sync(~0u, ok);
-    for (int u = 0; u < 32; ++u) {
-      const float du = __shfl_sync(~0u, ds, u);
-      if (!(kept >> u & 1)) continue;
-      const __nv_bfloat16* k = p.K + (j0 + u) * p.k_row + hk * p.k_head;
+  if (flags && threadIdx.x == 0 && block == 0 && split == 0 && hk == 0) atomicOr(p.status, flags);
+  const int ftok = kTile / p.r, mtok = kMove / p.r;  // query tokens of a fixed and of a moving tile
+  const int f0 = KEYS ? k0 + block * kTile : q0 + block * ftok;
+  const int f1 = KEYS ? k1 : q1;
+  const int left = (flags & SVCONV_STATUS_BAD_OFFSETS) ? 0 : KEYS ? min(kTile, f1 - f0) : min(ftok, f1 - f0) * p.r;  // rows
+  const int mstep = KEYS ? mtok : kMove;
+  const int tiles = KEYS ? (q1 - q0 + mtok - 1) / mtok : (k1 - k0 + kMove - 1) / kMove;
+  const int t_lo = (int)((int64_t)tiles * split / splits), t_hi = (int)((int64_t)tiles * (split + 1) / splits);
+  const int nt = left > 0 ? t_hi - t_lo : 0;
+  const int m0 = (KEYS ? q0 : k0) + t_lo * mstep;  // first row of the first moving tile
+  auto steps_of = [&](int s) { return (nt + 1 - s) / 2; };
+  // rows of moving tile t that take part (two words), and whether any is missing
+  auto partial = [&](int t) {
+    return KEYS ? (mtok * p.r < kMove || m0 + (t + 1) * mtok > q1) : (p.keep || m0 + (t + 1) * kMove > k1);
+  };
+  auto kept = [&](int t, uint32_t (&w)[2]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (lane + 32 * c < p.d) acc[c] = fmaf(du, __bfloat162float(k[lane + 32 * c]), acc[c]);
+    for (int i = 0; i < 2; ++i) {
+      const int at = 32 * i + lane;
+      bool on;
+      if constexpr (KEYS) {
+        on = at < min(mtok, q1 - m0 - t * mtok) * p.r;
+      } else {
+        const int j = m0 + t * kMove + at;
+        on = j < k1 && (!p.keep || __ldg(p.keep + j) != 0);
+      }
+      w[i] = __ballot_sync(0xffffffffu, on);
+    }
+  };
+  // first entry of the tile's statistics; the copy starts at the even entry before it
+  auto stat_of = [&](int t) { return (int64_t)hk * p.nq * p.r + (int64_t)(m0 + t * mtok) * p.r; };
+
+  int loaded = 0;
+  if (warp == kLoadWarp) {
+    if (lane == 0 && nt > 0) {
+      const CUtensorMap* f[2] = {KEYS ? &p.fk : &p.fq, KEYS ? &p.fv : &p.fdo};
+      const CUtensorMap* m[2] = {KEYS ? &p.mq : &p.mk, KEYS ? &p.mdo : &p.mv};
+      const uint32_t f_bytes = (uint32_t)(KEYS ? kTile : ftok * p.r) * 128u, m_bytes = (uint32_t)(KEYS ? mtok * p.r : kMove) * 128u;
+      mbar_arrive_expect_tx(&bar->ffull, 2 * DB * f_bytes);
+      for (int o = 0; o < 2; ++o)
+        for (int b = 0; b < DB; ++b) {
+          const uint32_t dst = sf + o * Sh::kFixedBytes + b * kBlockBytes;
+          if constexpr (KEYS) tma_load_3d(dst, f[o], &bar->ffull, b * 64, hk, f0);
+          else tma_load_4d(dst, f[o], &bar->ffull, b * 64, 0, hk, f0);
+        }
+      for (; loaded < nt; ++loaded) {
+        const int slot = loaded % NS;
+        if (loaded >= NS && !mbar_wait(&bar->mempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err, kDefaultTimeoutNs)) break;
+        mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * m_bytes + (KEYS ? 528u : 0u));
+        for (int o = 0; o < 2; ++o)
+          for (int b = 0; b < DB; ++b) {
+            const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
+            if constexpr (KEYS) tma_load_4d(dst, m[o], &bar->mfull[slot], b * 64, 0, hk, m0 + loaded * mtok);
+            else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
+          }
+        if constexpr (KEYS)
+          bulk_copy_g2s(sstat + slot * kStatBytes, p.stat + (stat_of(loaded) & ~(int64_t)1), 528u, &bar->mfull[slot]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (nt > 0) {
+      const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
+      const uint32_t idesc_s = idesc_bf16_f32(kTile, kMove, 0, 0), idesc_a = idesc_bf16_f32(kTile, dn, 0, 1);
+      bool ok = warp_wait(&bar->ffull, 0, abort_flag, err);
+      // operand o of the scores of tile t into column col
+      auto scores = [&](int o, int t, int col) {
+        const uint64_t a0 = smem_desc_sw128(sf + o * Sh::kFixedBytes, 16, 1024);
+        const uint64_t b0 = smem_desc_sw128(sm + (t % NS) * Sh::kStageBytes + o * Sh::kMoveBytes, 16, 1024);
+        for (int k = 0; k < ks; ++k)
+          tc_mma_bf16(tmem + col, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2),
+                      b0 + (uint64_t)((k >> 2) * (kMoveBlock >> 4) + (k & 3) * 2), idesc_s, k ? 1u : 0u);
+      };
+      // acc += A (tensor memory) x operand o of tile t
+      auto sums = [&](int o, int t, int a_col, int acc) {
+        const uint64_t b0 = smem_desc_sw128(sm + (t % NS) * Sh::kStageBytes + o * Sh::kMoveBytes, kMoveBlock, 1024);
+#pragma unroll
+        for (int k = 0; k < kMove / 16; ++k)
+          tc_mma_bf16_ts(tmem + acc, tmem + a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_a, (t | k) ? 1u : 0u);
+      };
+      auto landed = [&](int t) {  // the tile is there, rows that take no part zeroed (they meet zero weights)
+        if (!warp_wait(&bar->mfull[t % NS], (t / NS) & 1, abort_flag, err)) return false;
+        if (partial(t)) {
+          uint32_t w[2];
+          kept(t, w);
+          w[0] = ~w[0], w[1] = ~w[1];
+          scrub_rows(sm + (t % NS) * Sh::kStageBytes, 2 * DB, kMoveBlock, w);
+        }
+        if (lane == 0) tc_fence_after();
+        return true;
+      };
+      for (int s = 0; s < 2 && ok; ++s)
+        if (steps_of(s) > 0) {
+          ok = landed(s);
+          if (ok && lane == 0) {
+            scores(0, s, Tm::S(s));
+            scores(1, s, Tm::dP(s));
+            tc_commit(&bar->sfull[s]);
+          }
+          __syncwarp();
+        }
+      for (int t = 0; t < nt && ok; ++t) {
+        const int s = t & 1, ph = (t >> 1) & 1, next = t + 2;
+        ok = warp_wait(&bar->pfull[s], ph, abort_flag, err);
+        if (!ok) break;
+        if (next < nt && !(ok = landed(next))) break;
+        if (lane == 0) {
+          tc_fence_after();
+          if constexpr (Tm::kShared) {
+            // P and dS lie in the columns of the next scores: each product is waited for before its
+            // columns are written, the other product keeping the pipe busy meanwhile
+            sums(1, t, Tm::P(s), Tm::kAcc1);
+            tc_commit(&bar->pdone[s]);
+            sums(0, t, Tm::dS(s), Tm::kAcc2);
+            tc_commit(&bar->adone[s]);
+            tc_commit(&bar->mempty[t % NS]);
+            if (next < nt) {
+              ok = mbar_wait(&bar->pdone[s], ph, abort_flag, err, kDefaultTimeoutNs);
+              if (ok) scores(0, next, Tm::S(s));
+              if (ok) ok = mbar_wait(&bar->adone[s], ph, abort_flag, err, kDefaultTimeoutNs);
+              if (ok) scores(1, next, Tm::dP(s));
+              if (ok) tc_commit(&bar->sfull[s]);
+            }
+          } else {
+            if (next < nt) {
+              scores(0, next, Tm::S(s));
+              scores(1, next, Tm::dP(s));
+              tc_commit(&bar->sfull[s]);
+            }
+            if constexpr (KEYS) sums(1, t, Tm::P(s), Tm::kAcc1);
+            sums(0, t, Tm::dS(s), Tm::kAcc2);
+            tc_commit(&bar->adone[s]);
+            tc_commit(&bar->mempty[t % NS]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0) {  // every issued product is complete before tensor memory is released
+        tc_commit(&bar->fin);
+        volatile int never = 0;
+        mbar_wait(&bar->fin, 0, &never, err, kDefaultTimeoutNs);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ P and dS: one thread per fixed row
+    const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const bool warp_on = (warp & 3) * 32 < left, row_on = row < left;
+    const int steps = steps_of(s);
+    float row_lse = INFINITY, row_d = 0.f;
+    if (!KEYS && row_on) {
+      const float2 st = p.stat[(int64_t)hk * p.nq * p.r + (int64_t)f0 * p.r + row];
+      row_lse = st.x, row_d = st.y;
+    }
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      const int t = 2 * i + s;
+      uint32_t w[2] = {~0u, ~0u};
+      const bool some = partial(t);
+      if (some) kept(t, w);
+      if (KEYS && !(ok = warp_wait(&bar->mfull[t % NS], (t / NS) & 1, abort_flag, err))) break;
+      if (!(ok = warp_wait(&bar->sfull[s], i & 1, abort_flag, err))) break;
+      if (i > 0 && !(ok = warp_wait(&bar->adone[s], (i - 1) & 1, abort_flag, err))) break;  // P and dS are free again
+      tc_fence_after();
+      if (warp_on) {
+        const float2* st = reinterpret_cast<const float2*>(stats + (t % NS) * kStatBytes) + (KEYS ? (int)(stat_of(t) & 1) : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t a[32], b[32];
+          tmem_ld_32x32b_x32(tmem + lanes + Tm::S(s) + h * 32, a);
+          tmem_ld_32x32b_x32(tmem + lanes + Tm::dP(s) + h * 32, b);
+          tmem_ld_wait();
+          if (some) {
+            // columns that take no part: weight 0 whatever the products left there
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float2 q = KEYS ? st[h * 32 + k] : make_float2(row_lse, row_d);
+              const bool on = w[h] >> k & 1u;
+              const float x = on ? ex2(fmaf(__uint_as_float(a[k]), p.c, -q.x)) : 0.f;
+              b[k] = on ? __float_as_uint(x * (__uint_as_float(b[k]) - q.y)) : 0u;
+              a[k] = __float_as_uint(x);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float2 q = KEYS ? st[h * 32 + k] : make_float2(row_lse, row_d);
+              const float x = ex2(fmaf(__uint_as_float(a[k]), p.c, -q.x));
+              b[k] = __float_as_uint(x * (__uint_as_float(b[k]) - q.y));
+              a[k] = __float_as_uint(x);
+            }
+          }
+          uint32_t u[16];
+          if constexpr (KEYS) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
+            tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, u);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = pack_bf16(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1]));
+          tmem_st_x16(tmem + lanes + Tm::dS(s) + h * 16, u);
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      warp_arrive(&bar->pfull[s]);
+    }
+    if (ok && nt > 0) ok = warp_wait(&bar->fin, 0, abort_flag, err);  // both streams' products are complete
+    tc_fence_after();
+    // key pass: warpgroup 0 writes dV and 1 dK; query pass: each half of dQ's channels
+    if (ok && warp_on) {
+      const int64_t rows = KEYS ? (int64_t)p.nkv * p.Hkv : (int64_t)p.nq * p.Hq;
+      const int64_t at = KEYS ? (int64_t)(f0 + row) * p.Hkv + hk : (int64_t)(f0 + row / p.r) * p.Hq + hk * p.r + row % p.r;
+      const bool live = nt > 0 && !(KEYS && p.keep && row_on && p.keep[f0 + row] == 0);
+      const float f = KEYS && s == 0 ? 1.f : p.scale;
+      __nv_bfloat16* out = KEYS ? (s == 0 ? p.dV : p.dK) : p.dQ;
+      float* part = KEYS ? (s == 0 ? p.part_v : p.part_k) : p.part_q;
+      const int acc = KEYS && s == 0 ? Tm::kAcc1 : Tm::kAcc2;
+      const int b_lo = KEYS ? 0 : s * DB, b_hi = KEYS ? 2 * DB : s * DB + DB;
+      for (int b = b_lo; b < b_hi; ++b) {
+        if (b * 32 >= p.d) break;
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld_32x32b_x32(tmem + lanes + acc + b * 32, o);
+          tmem_ld_wait();
+        }
+        if (!row_on) continue;
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = live ? __uint_as_float(o[k]) * f : 0.f;
+        if (splits > 1) {
+          float* dst = part + (split * rows + at) * p.d + b * 32;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            if (b * 32 + k < p.d) *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else {
+          __nv_bfloat16* dst = out + at * p.d + b * 32;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            if (b * 32 + k < p.d)
+              *reinterpret_cast<uint4*>(dst + k) = make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]),
+                                                              pack_bf16(v[k + 4], v[k + 5]), pack_bf16(v[k + 6], v[k + 7]));
+        }
+      }
     }
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < p.d) p.dQ[at * p.d + lane + 32 * c] = __float2bfloat16(acc[c] * p.scale);
+  tc_fence_before();
+  __syncthreads();
+  if (bar->abort_flag && warp == kLoadWarp && lane == 0 && nt > 0) {
+    // a wait ran out somewhere: let the copies in flight land before the CTA gives its memory back
+    volatile int never = 0;
+    mbar_wait(&bar->ffull, 0, &never, err, kDefaultTimeoutNs);
+    for (int i = loaded > NS ? loaded - NS : 0; i < loaded; ++i)
+      mbar_wait(&bar->mfull[i % NS], (i / NS) & 1, &never, err, kDefaultTimeoutNs);
+  }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) attn_dkv_kernel(const __grid_constant__ AttnParams p) {
-  __shared__ float sk[kWarps][kMaxD], sv[kWarps][kMaxD];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int g = blockIdx.z, hk = blockIdx.y;
-  int q0, q1, k0, k1;
-  const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
-  if (flags & SVCONV_STATUS_BAD_OFFSETS) return;
-  const int row = k0 + blockIdx.x * kWarps + w;
-  if (row >= k1) return;
-  const bool on = !p.keep || p.keep[row];
-  float dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  if (on) {
-    for (int c = lane; c < p.d; c += 32) {
-      sk[w][c] = __bfloat162float(p.K[row * p.k_row + hk * p.k_head + c]) * (p.scale * kLog2e);
-      sv[w][c] = __bfloat162float(p.V[row * p.v_row + hk * p.v_head + c]);
+template <int DB>
+__global__ void __launch_bounds__(kFwdThreads, 1) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
+  using Sh = BwdShape<DB>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
+  const uint8_t* stats = aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)Sh::kStageBytes;
+  BwdBarriers* bar = reinterpret_cast<BwdBarriers*>(aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)(Sh::kStageBytes + kStatBytes));
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar->ffull, 1);
+    for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4);
+      mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
     }
-    __syncwarp();
-    const int n = (q1 - q0) * p.r;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      float pr = 0.f, ds = 0.f;
-      if (i < n) {
-        const int qi = q0 + i / p.r, h = hk * p.r + i % p.r;
-        const int64_t at = (int64_t)qi * p.Hq + h;
-        pr = exp2f(dot_row(sk[w], p.Q + qi * p.q_row + h * p.q_head, p.d) - p.lse[at] * kLog2e);
-        ds = pr * (dot_row(sv[w], p.dO + at * p.d, p.d) - p.D[at]);
-      }
-      for (int u = 0; u < 32 && i0 + u < n; ++u) {
-        const float pu = __shfl_sync(~0u, pr, u), du = __shfl_sync(~0u, ds, u);
-        const int qi = q0 + (i0 + u) / p.r, h = hk * p.r + (i0 + u) % p.r;
-        const __nv_bfloat16* q = p.Q + qi * p.q_row + h * p.q_head;
-        const __nv_bfloat16* go = p.dO + ((int64_t)qi * p.Hq + h) * p.d;
+    mbar_init(&bar->fin, 1);
+    bar->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bar->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < p.q_items) bwd_pass<DB, false>(p, blockIdx.x, base, bar, stats);
+  else bwd_pass<DB, true>(p, blockIdx.x - p.q_items, base, bar, stats);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// lse in base 2 and D = dO . O of every (query token, head), in the order of the packed rows of a key
+// head; 2^k lanes a row, 8 channels a lane.
+__global__ void __launch_bounds__(256) attn_stat_kernel(const __nv_bfloat16* __restrict__ dO, const __nv_bfloat16* __restrict__ O,
+                                                        const float* __restrict__ lse, int nq, int Hq, int r, int d, int lanes,
+                                                        float2* __restrict__ stat) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / lanes;
+  const int sub = threadIdx.x & (lanes - 1);
+  const bool on = row < (int64_t)nq * Hq;
+  float v = 0.f;
+  if (on && sub * 8 < d) {
+    const uint4 a = *reinterpret_cast<const uint4*>(dO + row * d + sub * 8), b = *reinterpret_cast<const uint4*>(O + row * d + sub * 8);
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (lane + 32 * c < p.d) {
-            dk[c] = fmaf(du, __bfloat162float(q[lane + 32 * c]), dk[c]);
-            dv[c] = fmaf(pu, __bfloat162float(go[lane + 32 * c]), dv[c]);
-          }
-      }
+    for (int i = 0; i < 4; ++i) {
+      v = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), v);
+      v = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), v);
     }
   }
-  const int64_t at = ((int64_t)row * p.Hkv + hk) * p.d;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < p.d) {
-      p.dK[at + lane + 32 * c] = __float2bfloat16(dk[c] * p.scale);
-      p.dV[at + lane + 32 * c] = __float2bfloat16(dv[c]);
-    }
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (on && sub == 0) {
+    const int64_t token = row / Hq;
+    const int h = (int)(row - token * Hq);
+    const float l = lse[row];
+    stat[(int64_t)(h / r) * nq * r + token * r + h % r] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, v);
+  }
+}
+
+// The splits of a gradient added in order: 8 channels a thread over the rows of group blockIdx.y.
+__global__ void __launch_bounds__(256) attn_sum_kernel(const float* __restrict__ part, int splits, const int32_t* off, const int32_t* off2,
+                                                       int n, int n2, int bound, int H, int d, __nv_bfloat16* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  int lo, hi, lo2, hi2;
+  const int flags = group_range(off, blockIdx.y, n, bound, lo, hi) | group_range(off2, blockIdx.y, n2, n2, lo2, hi2);
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if ((flags & SVCONV_STATUS_BAD_OFFSETS) || i >= (int64_t)(hi - lo) * H * d) return;
+  const int64_t at = (int64_t)lo * H * d + i, step = (int64_t)n * H * d;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = *reinterpret_cast<const float4*>(part + s * step + at), b = *reinterpret_cast<const float4*>(part + s * step + at + 4);
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  *reinterpret_cast<uint4*>(out + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 // ---------------------------------------------------------------------------- host side
@@ -686,7 +972,7 @@ int check_desc(const svconv_cross_attn_desc* c, svconv_cross_attn_desc& o) {
   o = *c;
   if (o.nq < 0 || o.nkv < 0 || o.G < 0 || o.max_q < 0 || o.max_kv < 0) return SVCONV_ERR_SIZE;
   if (o.Hq < 1 || o.Hkv < 1 || o.Hq > 65535 || o.G > 65535) return SVCONV_ERR_SIZE;
-  if (o.d < 8 || o.d > kMaxD || o.d % 8 != 0 || o.Hq % o.Hkv != 0 || o.Hq / o.Hkv > 128) return SVCONV_ERR_UNSUPPORTED;
+  if (o.d < 8 || o.d > kMaxD || o.d % 8 != 0 || o.Hq % o.Hkv != 0 || o.Hq / o.Hkv > kMove) return SVCONV_ERR_UNSUPPORTED;
   if (!std::isfinite(o.scale)) return SVCONV_ERR_SIZE;
   if (o.G > 0 && (!o.q_off || !o.kv_off)) return SVCONV_ERR_NULL;
   if (!fix_strides(o.q_row, o.q_head, o.nq, o.Hq, o.d) || !fix_strides(o.k_row, o.k_head, o.nkv, o.Hkv, o.d) ||
@@ -695,18 +981,6 @@ int check_desc(const svconv_cross_attn_desc* c, svconv_cross_attn_desc& o) {
   if (o.max_q > o.nq) o.max_q = o.nq;
   if (o.max_kv > o.nkv) o.max_kv = o.nkv;
   return SVCONV_OK;
-}
-
-AttnParams make_params(const svconv_cross_attn_desc& c, const void* Q, const void* K, const void* V, int* status) {
-  AttnParams p{};
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.K = static_cast<const __nv_bfloat16*>(K);
-  p.V = static_cast<const __nv_bfloat16*>(V);
-  p.q_row = c.q_row, p.q_head = c.q_head, p.k_row = c.k_row, p.k_head = c.k_head, p.v_row = c.v_row, p.v_head = c.v_head;
-  p.nq = c.nq, p.nkv = c.nkv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = c.Hq / c.Hkv, p.d = c.d, p.G = c.G;
-  p.q_off = c.q_off, p.kv_off = c.kv_off, p.max_q = c.max_q, p.max_kv = c.max_kv, p.keep = c.kv_keep, p.scale = c.scale;
-  p.status = status ? status : device_error_word();
-  return p;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -775,6 +1049,39 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
   return f;
 }
 
+// The same for the two passes of the backward call.
+struct BwdPlan {
+  int qblocks, qsplits, kblocks, ksplits;
+  size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
+  size_t floats() const { return stat + pq + 2 * pk; }
+};
+int bwd_splits(long long units, int tiles) {
+  const int most = cdiv(tiles, 2 * kMinTiles);
+  const int s = units >= kSms ? 1 : (int)(kSms / units);
+  return s > most ? (most < 1 ? 1 : most) : s;
+}
+BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
+  BwdPlan b;
+  const int r = c.Hq / c.Hkv;
+  b.qblocks = cdiv(c.max_q, kTile / r);
+  b.kblocks = cdiv(c.max_kv, kTile);
+  const long long heads = (long long)c.G * c.Hkv;
+  b.qsplits = b.qblocks ? bwd_splits(heads * b.qblocks, cdiv(c.max_kv, kMove)) : 1;
+  b.ksplits = b.kblocks ? bwd_splits(heads * b.kblocks, cdiv(c.max_q, kMove / r)) : 1;
+  const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
+  b.stat = ((nq + 2 + kMove) * 2 + 3) / 4 * 4;  // a tile's copy may run past the last row
+  b.pq = b.qsplits > 1 ? b.qsplits * nq * c.d : 0;
+  b.pk = b.ksplits > 1 ? b.ksplits * nk * c.d : 0;
+  return b;
+}
+
+template <int DB>
+cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t s) {
+  static int done[64];
+  cudaError_t e = ensure_smem_attr(attn_bwd_kernel<DB>, BwdShape<DB>::kSmem, done);
+  return e == cudaSuccess ? launch_pdl(attn_bwd_kernel<DB>, dim3(grid), dim3(kFwdThreads), BwdShape<DB>::kSmem, s, p) : e;
+}
+
 template <int DB>
 cudaError_t launch_fwd(const FwdParams& p, int grid, cudaStream_t s) {
   static int done[64];
@@ -798,8 +1105,8 @@ size_t svconv_cross_attn_fwd_workspace_size(const svconv_cross_attn_desc* desc) 
 
 size_t svconv_cross_attn_bwd_workspace_size(const svconv_cross_attn_desc* desc) {
   svconv_cross_attn_desc c;
-  if (check_desc(desc, c)) return 0;
-  return ((size_t)c.nq * c.Hq * sizeof(float) + 15) / 16 * 16;
+  if (check_desc(desc, c) || c.G == 0) return 0;
+  return plan_bwd(c).floats() * sizeof(float);
 }
 
 int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, const void* K, const void* V, void* O,
@@ -854,18 +1161,60 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   const size_t need = svconv_cross_attn_bwd_workspace_size(desc);
   if (need && (!workspace || ws_bytes < need)) return SVCONV_ERR_WORKSPACE;
   if ((rc = check_device())) return rc;
-  AttnParams p = make_params(c, Q, K, V, dev_status);
-  p.O = static_cast<const __nv_bfloat16*>(O);
-  p.dO = static_cast<const __nv_bfloat16*>(dO);
-  p.lse = lse;
+  const BwdPlan b = plan_bwd(c);
+  const long long heads = (long long)c.G * c.Hkv;
+  const long long q_items = heads * b.qblocks * b.qsplits, k_items = heads * b.kblocks * b.ksplits;
+  const int r = c.Hq / c.Hkv;
+  int lanes = 1;
+  while (lanes < c.d / 8) lanes *= 2;
+  const long long stat_grid = ((long long)c.nq * c.Hq * lanes + 255) / 256;
+  if (q_items + k_items > 0x7fffffffLL || stat_grid > 0x7fffffffLL) return SVCONV_ERR_SIZE;
+  float* ws = static_cast<float*>(workspace);
+  BwdParams p{};
+  p.q_off = c.q_off, p.kv_off = c.kv_off, p.keep = c.kv_keep;
+  p.nq = c.nq, p.nkv = c.nkv, p.max_q = c.max_q, p.max_kv = c.max_kv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = r, p.d = c.d;
+  p.qblocks = b.qblocks, p.qsplits = b.qsplits, p.kblocks = b.kblocks, p.ksplits = b.ksplits;
+  p.q_items = (int)q_items;
+  p.c = c.scale * kLog2e;
+  p.scale = c.scale;
+  float2* stat = reinterpret_cast<float2*>(ws);
+  p.stat = stat;
+  p.part_q = ws + b.stat;
+  p.part_k = p.part_q + b.pq;
+  p.part_v = p.part_k + b.pk;
   p.dQ = static_cast<__nv_bfloat16*>(dQ);
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
-  p.D = static_cast<float*>(workspace);
+  p.status = dev_status ? dev_status : device_error_word();
+  // a side without rows: its maps only have to be well formed
+  const void *q = c.nq ? Q : K, *go = c.nq ? dO : K, *k = c.nkv ? K : Q, *v = c.nkv ? V : Q;
+  const int64_t go_row = (int64_t)c.Hq * c.d, go_head = c.d;
+  if (!make_packed_map(&p.fq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, kTile / r) ||
+      !make_packed_map(&p.mq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, kMove / r) ||
+      !make_packed_map(&p.fdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, kTile / r) ||
+      !make_packed_map(&p.mdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, kMove / r) ||
+      !make_rows_map(&p.fk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kTile) ||
+      !make_rows_map(&p.mk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kMove) ||
+      !make_rows_map(&p.fv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kTile) ||
+      !make_rows_map(&p.mv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kMove))
+    return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  if (c.max_q > 0) attn_dq_kernel<<<dim3(cdiv(c.max_q, kWarps), c.Hq, c.G), kWarps * 32, 0, s>>>(p);
-  if (c.max_kv > 0) attn_dkv_kernel<<<dim3(cdiv(c.max_kv, kWarps), c.Hkv, c.G), kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SVCONV_OK : SVCONV_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (c.nq > 0)
+    e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
+                   static_cast<const __nv_bfloat16*>(O), lse, c.nq, c.Hq, r, c.d, lanes, stat);
+  if (e == cudaSuccess)
+    e = c.d <= 64 ? launch_bwd<1>(p, (int)(q_items + k_items), s) : launch_bwd<2>(p, (int)(q_items + k_items), s);
+  auto add = [&](const float* part, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound, int H,
+                 __nv_bfloat16* out) {
+    if (e != cudaSuccess || splits < 2) return;
+    const long long grid = ((long long)bound * H * c.d / 8 + 255) / 256;
+    e = launch_pdl(attn_sum_kernel, dim3((unsigned)grid, c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out);
+  };
+  add(p.part_q, b.qsplits, c.q_off, c.kv_off, c.nq, c.nkv, c.max_q, c.Hq, p.dQ);
+  add(p.part_k, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dK);
+  add(p.part_v, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dV);
+  return e == cudaSuccess ? SVCONV_OK : SVCONV_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -148,7 +148,8 @@ CASES = [
     ((2, 30), (6000, 4100), 8, 1, 128, 1.0, 0, False),
     ((1100,), (30,), 2, 2, 72, 1.0, 0, False),
     ((385, 700), (513, 900), 2, 1, 128, 0.8, 0, False),
-    ((20,), (60,), 128, 1, 64, 1.0, 0, False),
+    ((20, 90), (60, 300), 64, 1, 64, 1.0, 0, False),
+    ((37,), (200,), 21, 1, 128, 1.0, 0, False),
     ((1,), (20000,), 4, 4, 64, 1.0, 0, False),
     ((2300,), (100,), 4, 4, 64, 1.0, 0, False),
 ]
