@@ -2,7 +2,7 @@
 //
 // HBM-bound: the norm reads every value once, the scaling reads and writes it once more (from L2
 // where the set fits).  The tensors travel as a table in the kernel parameters, cut into chunks of
-// kClipChunk values; CTAs stride over the chunks of all tensors, so many small tensors cost no
+// kClipChunk values; each CTA takes one run of the chunks of all tensors, so many small tensors cost no
 // launches of their own.  Squares are summed in fp64: a finite set of gradients has a finite
 // norm, and one conversion per value stays below the time of its load.  CTA sums are added in a
 // fixed order by every CTA of the second kernel (deterministic, no atomics).
@@ -19,7 +19,8 @@ namespace {
 
 constexpr int kClipThreads = 256;
 constexpr int kClipCtas = 592;      // 4 per SM on 148 SMs
-constexpr int kClipChunk = 8192;    // values of one tensor per step of a CTA
+constexpr int kClipChunk = 4096;    // values of one tensor per step of a CTA
+constexpr int kClipBatch = 4;       // 16-byte loads in flight per thread
 constexpr int kClipSmall = 64;      // tensors in the small table (2.5 KB of parameters)
 constexpr int kClipLarge = 800;     // tensors in the large one (under the 32,764 bytes a launch may carry)
 
@@ -45,6 +46,12 @@ __device__ __forceinline__ int tensor_of(const ClipTable<N>& t, int chunk) {
     if (t.first[mid] <= chunk) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// CTA b takes chunks first_of(b) .. first_of(b + 1) - 1: one run of the table, found once.
+template <int N>
+__device__ __forceinline__ int first_of(const ClipTable<N>& t, int b) {
+  return (int)((int64_t)t.first[t.count] * b / (int)gridDim.x);
 }
 
 __device__ __forceinline__ float value(const float* p) { return *p; }
@@ -83,15 +90,20 @@ __device__ __forceinline__ double squares(const T* p, int n) {
     a = fma(x, x, a);
   }
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vecs; i += kClipThreads) {
-    float f[V];
-    widen16<T>(q[i], f);
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += kClipBatch * kClipThreads) {
+    uint4 u[kClipBatch];
 #pragma unroll
-    for (int j = 0; j < V; j += 2) {
-      const double x = f[j], y = f[j + 1];
-      a = fma(x, x, a);
-      b = fma(y, y, b);
+    for (int k = 0; k < kClipBatch; ++k) u[k] = i0 + k * kClipThreads < vecs ? q[i0 + k * kClipThreads] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < kClipBatch; ++k) {
+      float f[V];
+      widen16<T>(u[k], f);
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        const double x = f[j], y = f[j + 1];
+        a = fma(x, x, a);
+        b = fma(y, y, b);
+      }
     }
   }
   for (int i = head + vecs * V + threadIdx.x; i < n; i += kClipThreads) {
@@ -113,13 +125,15 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(const __grid_constant__ ClipTable<N> t) {
+__global__ void __launch_bounds__(kClipThreads, 4) clip_norm_kernel(const __grid_constant__ ClipTable<N> t) {
   __shared__ double s[kClipThreads / 32];
   pdl_wait();
   pdl_trigger();
   double sum = 0.0;
-  for (int c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
+  const int lo = first_of(t, blockIdx.x), hi = first_of(t, blockIdx.x + 1);
+  int i = lo < hi ? tensor_of(t, lo) : 0;
+  for (int c = lo; c < hi; ++c) {
+    while (c >= t.first[i + 1]) ++i;
     const int64_t at = (int64_t)(c - t.first[i]) * kClipChunk;
     const int n = (int)min((int64_t)kClipChunk, t.numel[i] - at);
     sum += t.bf16[i] ? squares(static_cast<const __nv_bfloat16*>(t.src[i]) + at, n)
@@ -137,27 +151,34 @@ __device__ __forceinline__ void scaled(T* dst, const T* src, int n, float f) {
   for (int i = threadIdx.x; i < head; i += kClipThreads) put(dst + i, value(src + i) * f);
   const uint4* q = reinterpret_cast<const uint4*>(src + head);
   uint4* o = reinterpret_cast<uint4*>(dst + head);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vecs; i += kClipThreads) {
-    float x[V];
-    widen16<T>(q[i], x);
-    uint32_t v[4];
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += kClipBatch * kClipThreads) {
+    uint4 u[kClipBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 4) {
-        v[j] = __float_as_uint(x[j] * f);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
-        v[j] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int k = 0; k < kClipBatch; ++k)
+      if (i0 + k * kClipThreads < vecs) u[k] = q[i0 + k * kClipThreads];
+#pragma unroll
+    for (int k = 0; k < kClipBatch; ++k) {
+      if (i0 + k * kClipThreads >= vecs) break;
+      float x[V];
+      widen16<T>(u[k], x);
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          v[j] = __float_as_uint(x[j] * f);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+          v[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
       }
+      __stcs(o + i0 + k * kClipThreads, make_uint4(v[0], v[1], v[2], v[3]));  // not read again here: leave L2 to the sources
     }
-    o[i] = make_uint4(v[0], v[1], v[2], v[3]);
   }
   for (int i = head + vecs * V + threadIdx.x; i < n; i += kClipThreads) put(dst + i, value(src + i) * f);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_constant__ ClipTable<N> t) {
+__global__ void __launch_bounds__(kClipThreads, 4) clip_scale_kernel(const __grid_constant__ ClipTable<N> t) {
   __shared__ double s[kClipThreads / 32];
   pdl_wait();
   pdl_trigger();
@@ -167,8 +188,10 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   if (blockIdx.x == 0 && threadIdx.x == 0) *t.norm = norm;
   float f = t.max_norm / (norm + 1e-6f);
   if (!(f < 1.f) || !(norm < INFINITY)) f = 1.f;
-  for (int c = gridDim.x - 1 - blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
+  const int lo = first_of(t, blockIdx.x), hi = first_of(t, blockIdx.x + 1);
+  int i = lo < hi ? tensor_of(t, hi - 1) : 0;
+  for (int c = hi - 1; c >= lo; --c) {  // backwards: what the norm read last is still in L2
+    while (c < t.first[i]) --i;
     if (f == 1.f && t.dst[i] == t.src[i]) continue;
     const int64_t at = (int64_t)(c - t.first[i]) * kClipChunk;
     const int n = (int)min((int64_t)kClipChunk, t.numel[i] - at);

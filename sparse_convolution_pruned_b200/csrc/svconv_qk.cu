@@ -1,13 +1,17 @@
 // Per-head RMS norm with rotary positions, forward and backward (svconv_qk_norm_rope_fwd / _bwd).
 //
 // HBM-bound: each value is read once and written once (backward: two reads, one write) for ~10
-// flops.  Both sides (queries and keys) share one launch, split over the CTAs by their bytes.  A
-// warp owns whole tokens: its lanes form the sines and cosines of a token's pairs once (angle in
-// fp64 turns, reduced to one turn, then sincospif) and share them over all heads through shared
-// memory; a head's d channels lie in d / 8 consecutive lanes (padded to a power of two), 8 per
-// lane, so a norm is a few shuffles and the partner of a half-layout pair sits rot / 16 lanes away.
-// Four 16-byte loads per lane are in flight before the trigonometry starts.  All arithmetic is
-// fp32 (angles fp64) and rounds once, at the store.
+// flops, so the work is to keep the instructions per value below what the loads take.  Both sides
+// (queries and keys) share one launch, split over the CTAs by their bytes.  A warp owns whole tokens: its
+// lanes form the sines and cosines of a token's pairs once and share them over all heads through shared
+// memory.  A head's d channels lie in d / 8 lanes (padded to a power of two), each lane holding both members
+// of its four pairs, so a norm is a few shuffles and a rotation none.  Four chunks per lane are in
+// flight before the trigonometry starts.
+//
+// Angles: a pair's frequency in turns per position is kept as a 64-bit binary fraction; its product with the
+// position, modulo one turn, is three integer operations and off by less than 2^-33 turns at any position.
+// All other arithmetic is fp32 and rounds once, at the store.  The bf16 forms take sin.approx /
+// cos.approx (error below 2^-20.9 on one turn, 2^-12 of a bf16 rounding), the fp32 forms sincospif.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -20,9 +24,10 @@ namespace svc {
 namespace {
 
 constexpr int kQkWarps = 8;
-constexpr int kQkCtas = 592;    // 4 per SM on 148 SMs: all resident, fixed so that dw partials need no device query
+constexpr int kQkSms = 148;     // fixed numbers, so that the partial sums of dw need no device query
+constexpr int kQkCtas = 4 * kQkSms;
 constexpr int kQkMaxD = 256;
-constexpr int kQkBatch = 4;     // 16-byte chunks in flight per lane
+constexpr int kQkBatch = 4;     // chunks (8 channels a lane) in flight
 constexpr int kQkMaxPairs = kQkMaxD / 2;
 
 struct QkSide {
@@ -44,19 +49,24 @@ struct QkParams {
   float* part;                     // backward: [ctas][d] partial sums of dw
 };
 
-// 8 consecutive channels as loaded: bf16 in 4 words, fp32 in 8
+// A lane's 8 channels of a head as loaded, from channels a and b on, four each: bf16 in 4 words, fp32 in 8
 template <typename T>
 struct Raw {
   uint32_t v[sizeof(T) * 2];
 };
 
-template <typename T>
-__device__ __forceinline__ Raw<T> load8(const T* p) {
+template <typename T, bool HALF>
+__device__ __forceinline__ Raw<T> load8(const T* p, int a, int b) {
   Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    r.v[4 * i] = u.x, r.v[4 * i + 1] = u.y, r.v[4 * i + 2] = u.z, r.v[4 * i + 3] = u.w;
+  if constexpr (sizeof(T) == 4) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p + a)), w = __ldcs(reinterpret_cast<const uint4*>(p + b));
+    r.v[0] = u.x, r.v[1] = u.y, r.v[2] = u.z, r.v[3] = u.w, r.v[4] = w.x, r.v[5] = w.y, r.v[6] = w.z, r.v[7] = w.w;
+  } else if constexpr (HALF) {
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p + a)), w = __ldcs(reinterpret_cast<const uint2*>(p + b));
+    r.v[0] = u.x, r.v[1] = u.y, r.v[2] = w.x, r.v[3] = w.y;
+  } else {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p + a));
+    r.v[0] = u.x, r.v[1] = u.y, r.v[2] = u.z, r.v[3] = u.w;
   }
   return r;
 }
@@ -75,22 +85,25 @@ __device__ __forceinline__ void widen(const Raw<T>& r, float (&f)[8]) {
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  uint32_t v[sizeof(T) * 2];
+template <typename T, bool HALF>
+__device__ __forceinline__ void store8(T* p, int a, int b, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(f[i]);
+    __stcs(reinterpret_cast<float4*>(p + a), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p + b), make_float4(f[4], f[5], f[6], f[7]));
   } else {
+    uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
       v[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
+    if constexpr (HALF) {
+      __stcs(reinterpret_cast<uint2*>(p + a), make_uint2(v[0], v[1]));
+      __stcs(reinterpret_cast<uint2*>(p + b), make_uint2(v[2], v[3]));
+    } else {
+      __stcs(reinterpret_cast<uint4*>(p + a), make_uint4(v[0], v[1], v[2], v[3]));
+    }
   }
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    __stcs(reinterpret_cast<uint4*>(p) + i, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
 }
 
 __device__ __forceinline__ float sum_lanes(float v, int lanes) {
@@ -98,57 +111,35 @@ __device__ __forceinline__ float sum_lanes(float v, int lanes) {
   return v;
 }
 
-__device__ __forceinline__ void lds4(const float* p, float* f) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-}
-
-// Turn (INVERSE: back) the lane's 8 channels of a head, from channel c0, by the angles in cs / sn.
+// Turn (INVERSE: back) the lane's four pairs by the angles at cs / sn: channels i and 4 + i, or 2i and 2i + 1.
 template <bool HALF, bool INVERSE>
-__device__ __forceinline__ void rotate(float (&f)[8], const float* cs, const float* sn, int c0, int pairs) {
-  const bool on = c0 < 2 * pairs;
-  if constexpr (HALF) {
-    const bool second = c0 >= pairs;
-    const int lane = threadIdx.x & 31;
-    const int mate = on ? (second ? lane - pairs / 8 : lane + pairs / 8) : lane;
-    const int p0 = on ? (second ? c0 - pairs : c0) : 0;
-    float c[8], s[8];
-    lds4(cs + p0, c), lds4(cs + p0 + 4, c + 4);
-    lds4(sn + p0, s), lds4(sn + p0 + 4, s + 4);
-    const float sign = (second != INVERSE) ? 1.f : -1.f;
+__device__ __forceinline__ void rotate(float (&f)[8], const float* cs, const float* sn) {
+  const float4 c4 = *reinterpret_cast<const float4*>(cs), s4 = *reinterpret_cast<const float4*>(sn);
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, f[i], mate);
-      if (on) f[i] = f[i] * c[i] + o * (sign * s[i]);
-    }
-  } else {
-    if (on) {
-      float c[4], s[4];
-      lds4(cs + c0 / 2, c);
-      lds4(sn + c0 / 2, s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float z = INVERSE ? -s[i] : s[i];
-        const float a = f[2 * i], b = f[2 * i + 1];
-        f[2 * i] = a * c[i] - b * z;
-        f[2 * i + 1] = a * z + b * c[i];
-      }
-    }
+  for (int i = 0; i < 4; ++i) {
+    float& a = f[HALF ? i : 2 * i];
+    float& b = f[HALF ? 4 + i : 2 * i + 1];
+    const float z = INVERSE ? -s[i] : s[i];
+    const float t = a * c[i] - b * z;
+    b = a * z + b * c[i];
+    a = t;
   }
 }
 
 // One warp's share of a side: TPB tokens of kQkBatch / TPB chunks each per step (TPB = 1: as many
 // steps per token as its chunks need).  dw gathers the lane's 8 channels of the weight gradient.
 template <typename T, bool HALF, bool BWD, int TPB>
-__device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, int cta, float* cs, float* sn, float (&dw)[8]) {
+__device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, int cta, const unsigned long long* turn, float* cs,
+                                          float* sn, float (&dw)[8]) {
   constexpr int CPB = kQkBatch / TPB;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (p.lanes - 1), hsub = lane / p.lanes, heads_per = 32 / p.lanes;
-  const int c0 = sub * 8;
-  const bool on = c0 < p.d;
+  const bool on = sub * 8 < p.d, turned = sub * 4 < p.pairs;
+  const int a = HALF && turned ? sub * 4 : sub * 8, b = HALF && turned ? a + p.pairs : a + 4;
   float w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = on ? (sd.w ? sd.w[c0 + i] : 1.f) : 0.f;
+  for (int i = 0; i < 8; ++i) w[i] = on ? (sd.w ? sd.w[i < 4 ? a + i : b + i - 4] : 1.f) : 0.f;
   const float inv_d = 1.f / (float)p.d;
   const T* x = static_cast<const T*>(sd.x);
   const T* dy = static_cast<const T*>(sd.dy);
@@ -158,18 +149,17 @@ __device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, i
     for (int ch0 = 0; ch0 < sd.chunks; ch0 += CPB) {
       Raw<T> rx[kQkBatch], rg[BWD ? kQkBatch : 1];
 #pragma unroll
-      for (int b = 0; b < kQkBatch; ++b) {
-        const int64_t t = t0 + b / CPB;
-        const int h = (ch0 + b % CPB) * heads_per + hsub;
-        const bool ok = on && t < sd.n && ch0 + b % CPB < sd.chunks && h < sd.H;
+      for (int u = 0; u < kQkBatch; ++u) {
+        const int64_t t = t0 + u / CPB;
+        const int h = (ch0 + u % CPB) * heads_per + hsub;
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
-          rx[b].v[i] = 0u;
-          if constexpr (BWD) rg[b].v[i] = 0u;
+          rx[u].v[i] = 0u;
+          if constexpr (BWD) rg[u].v[i] = 0u;
         }
-        if (ok) {
-          rx[b] = load8(x + t * sd.x_row + (int64_t)h * p.d + c0);
-          if constexpr (BWD) rg[b] = load8(dy + (t * sd.H + h) * p.d + c0);
+        if (on && t < sd.n && h < sd.H) {
+          rx[u] = load8<T, HALF>(x + t * sd.x_row + h * p.d, a, b);
+          if constexpr (BWD) rg[u] = load8<T, HALF>(dy + (t * sd.H + h) * p.d, a, b);
         }
       }
       if (ch0 == 0) {
@@ -179,39 +169,44 @@ __device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, i
           const int tt = TPB == 1 ? 0 : i / p.pairs, pr = TPB == 1 ? i : i - tt * p.pairs;
           if (t0 + tt < sd.n) {
             const int axis = pr < p.cut1 ? 0 : pr < p.cut2 ? 1 : 2;
-            const double turns = (double)sd.pos[(t0 + tt) * p.axes + axis] * p.freq[pr] * 0.15915494309189533577;
-            const float f = (float)(turns - rint(turns));
-            float a, c;
-            sincospif(2.f * f, &a, &c);
-            cs[i] = c;
-            sn[i] = a;
+            const int pos = sd.pos[(t0 + tt) * p.axes + axis];
+            const unsigned long long f = turn[pr];
+            const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
+            const uint32_t frac = hi * (uint32_t)pos + __umulhi(lo, (uint32_t)pos) - (pos < 0 ? lo : 0u);
+            const float turns = (float)(int)frac * 2.3283064365386963e-10f;  // 2^-32: -1/2 .. 1/2
+            if constexpr (sizeof(T) == 4) {
+              sincospif(2.f * turns, &sn[i], &cs[i]);
+            } else {
+              sn[i] = __sinf(6.283185307179586f * turns);
+              cs[i] = __cosf(6.283185307179586f * turns);
+            }
           }
         }
         __syncwarp();
       }
 #pragma unroll
-      for (int b = 0; b < kQkBatch; ++b) {
-        const int64_t t = t0 + b / CPB;
-        const int h = (ch0 + b % CPB) * heads_per + hsub;
-        if (t >= sd.n || ch0 + b % CPB >= sd.chunks) continue;  // uniform over the warp
+      for (int u = 0; u < kQkBatch; ++u) {
+        const int64_t t = t0 + u / CPB;
+        const int h = (ch0 + u % CPB) * heads_per + hsub;
+        if (t >= sd.n || ch0 + u % CPB >= sd.chunks) continue;  // uniform over the warp
         const bool ok = on && h < sd.H;
         float f[8];
-        widen(rx[b], f);
+        widen(rx[u], f);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        const float rstd = 1.f / sqrtf(sum_lanes(ss, p.lanes) * inv_d + p.eps);
-        const float* tcs = cs + (b / CPB) * p.pairs;
-        const float* tsn = sn + (b / CPB) * p.pairs;
+        const float rstd = rsqrtf(sum_lanes(ss, p.lanes) * inv_d + p.eps);
+        const float* tcs = cs + (u / CPB) * p.pairs + sub * 4;
+        const float* tsn = sn + (u / CPB) * p.pairs + sub * 4;
         if constexpr (!BWD) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
-          rotate<HALF, false>(f, tcs, tsn, c0, p.pairs);
-          if (ok) store8(out + (t * sd.H + h) * p.d + c0, f);
+          if (turned) rotate<HALF, false>(f, tcs, tsn);
+          if (ok) store8<T, HALF>(out + (t * sd.H + h) * p.d, a, b, f);
         } else {
           float g[8];
-          widen(rg[b], g);
-          rotate<HALF, true>(g, tcs, tsn, c0, p.pairs);
+          widen(rg[u], g);
+          if (turned) rotate<HALF, true>(g, tcs, tsn);
           float dot = 0.f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -223,21 +218,31 @@ __device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, i
           dot = sum_lanes(dot, p.lanes) * inv_d;
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] = rstd * (g[i] - f[i] * dot);
-          if (ok) store8(out + (t * sd.H + h) * p.d + c0, g);
+          if (ok) store8<T, HALF>(out + (t * sd.H + h) * p.d, a, b, g);
         }
       }
     }
   }
 }
 
+// CTAs resident on an SM: as many as the registers of a variant allow without spills.
+template <typename T, bool BWD>
+constexpr int kQkPerSm = BWD ? (sizeof(T) == 4 ? 2 : 3) : (sizeof(T) == 4 ? 3 : 4);
+
 // CTAs 0 .. side[0].ctas-1 take the queries, the rest the keys; a side's warps stride over its tokens.
 template <typename T, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kQkWarps * 32, BWD || sizeof(T) == 4 ? 2 : 3) qk_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQkWarps * 32, kQkPerSm<T, BWD>) qk_kernel(const __grid_constant__ QkParams p) {
   __shared__ __align__(16) float s_cs[kQkWarps][kQkBatch * kQkMaxPairs];
   __shared__ __align__(16) float s_sn[kQkWarps][kQkBatch * kQkMaxPairs];
+  __shared__ unsigned long long s_turn[kQkMaxPairs];
   const int warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
+  if ((int)threadIdx.x < p.pairs) {
+    const double t = p.freq[threadIdx.x] * 0.15915494309189533577;
+    s_turn[threadIdx.x] = (unsigned long long)__double2ll_rn((t - rint(t)) * 18446744073709551616.0);
+  }
+  __syncthreads();
   const bool is_k = (int)blockIdx.x >= p.side[0].ctas;
   const QkSide& sd = p.side[is_k ? 1 : 0];
   const int cta = (int)blockIdx.x - (is_k ? p.side[0].ctas : 0);
@@ -245,11 +250,11 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD || sizeof(T) == 4 ? 2 : 3) 
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = 0.f;
   if (sd.chunks == 1)
-    qk_tokens<T, HALF, BWD, 4>(p, sd, cta, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, 4>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   else if (sd.chunks == 2)
-    qk_tokens<T, HALF, BWD, 2>(p, sd, cta, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, 2>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   else
-    qk_tokens<T, HALF, BWD, 1>(p, sd, cta, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, 1>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   if constexpr (BWD) {
     // dw of this CTA: warps and head slots in a fixed order
     __shared__ float s_dw[kQkWarps][32][8];
@@ -257,9 +262,15 @@ __global__ void __launch_bounds__(kQkWarps * 32, BWD || sizeof(T) == 4 ? 2 : 3) 
     for (int i = 0; i < 8; ++i) s_dw[warp][threadIdx.x & 31][i] = dw[i];
     __syncthreads();
     for (int c = threadIdx.x; c < p.d; c += kQkWarps * 32) {
+      // the lane and place that held channel c
+      int sub = c / 8, at = c % 8;
+      if (HALF && c < 2 * p.pairs) {
+        const int m = c < p.pairs ? c : c - p.pairs;
+        sub = m / 4, at = m % 4 + (c < p.pairs ? 0 : 4);
+      }
       float s = 0.f;
       for (int v = 0; v < kQkWarps; ++v)
-        for (int h = 0; h < 32 / p.lanes; ++h) s += s_dw[v][h * p.lanes + c / 8][c % 8];
+        for (int h = 0; h < 32 / p.lanes; ++h) s += s_dw[v][h * p.lanes + sub][at];
       p.part[(size_t)blockIdx.x * p.d + c] = s;
     }
   }
@@ -287,31 +298,33 @@ __global__ void __launch_bounds__(256) qk_dw_kernel(const float* part, int d, in
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// CTAs of each side: as many as its tokens can use, at most kQkCtas in all, shared by bytes.
-void split_ctas(QkParams& p) {
+// CTAs of each side: as many as its tokens can use, at most `cap` in all, shared by bytes.
+void split_ctas(QkParams& p, int cap) {
   int need[2];
   double bytes[2];
   for (int i = 0; i < 2; ++i) {
     const QkSide& s = p.side[i];
     const int tpb = s.chunks == 1 ? 4 : s.chunks == 2 ? 2 : 1;
     const int64_t c = ((int64_t)s.n + kQkWarps * tpb - 1) / (kQkWarps * tpb);
-    need[i] = c > kQkCtas ? kQkCtas : (int)c;
+    need[i] = c > cap ? cap : (int)c;
     bytes[i] = (double)s.n * s.H;
   }
-  if (need[0] + need[1] > kQkCtas) {
-    int a = (int)(kQkCtas * (bytes[0] / (bytes[0] + bytes[1])) + 0.5);
+  if (need[0] + need[1] > cap) {
+    int a = (int)(cap * (bytes[0] / (bytes[0] + bytes[1])) + 0.5);
     if (a < 1 && need[0] > 0) a = 1;
-    if (a > kQkCtas - 1 && need[1] > 0) a = kQkCtas - 1;
+    if (a > cap - 1 && need[1] > 0) a = cap - 1;
     if (a > need[0]) a = need[0];
     need[0] = a;
-    if (need[1] > kQkCtas - a) need[1] = kQkCtas - a;
+    if (need[1] > cap - a) need[1] = cap - a;
   }
   p.side[0].ctas = need[0];
   p.side[1].ctas = need[1];
 }
 
 template <typename T, bool HALF, bool BWD>
-cudaError_t launch_qk(const QkParams& p, cudaStream_t s) {
+cudaError_t launch_qk(QkParams& p, cudaStream_t s) {
+  static_assert(kQkSms * kQkPerSm<T, BWD> <= kQkCtas, "the partial sums have kQkCtas slots");
+  split_ctas(p, kQkSms * kQkPerSm<T, BWD>);
   const int grid = p.side[0].ctas + p.side[1].ctas;
   return grid == 0 ? cudaSuccess : launch_pdl(qk_kernel<T, HALF, BWD>, dim3(grid), dim3(kQkWarps * 32), 0, s, p);
 }
@@ -366,7 +379,6 @@ int qk_run(bool bwd, int dtype, int d, int rot, int layout, const double* freq, 
   while (p.lanes < d / 8) p.lanes *= 2;
   const int heads_per = 32 / p.lanes;
   for (QkSide& sd : p.side) sd.chunks = (sd.H + heads_per - 1) / heads_per;
-  split_ctas(p);
   p.eps = eps;
   p.part = static_cast<float*>(workspace);
   cudaError_t e;

@@ -11,7 +11,10 @@ the input's device.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
+import itertools
 import os
 import re
 from typing import Optional, Sequence, Tuple
@@ -395,65 +398,96 @@ def svconv_adapter_fwd_xattn(X: torch.Tensor, nbr: torch.Tensor, frame_off: torc
     return X, aux_out
 
 
-def _heads_first(name: str, t: torch.Tensor):
-    """[n, H, d] bf16 with contiguous channels; rows and heads may be strided (a slice of a fused projection)."""
-    if not t.is_cuda:
+def _device_of(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("svconv operates on CUDA tensors only")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: bf16 is needed, got {t.dtype}")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name}: [rows, heads, channels] with contiguous channels is needed")
+    return index
 
 
-def _like(name: str, t: torch.Tensor, shape, dtype, dev):
-    _cuda(t)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name}: {tuple(shape)} {dtype} on {dev} is needed, got {tuple(t.shape)} {t.dtype} on {t.device}")
+def _current(index: int):
+    """Makes device `index` current for a call: launches and device queries go to the current device."""
+    return _SAME_DEVICE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _ensure(name: str, t: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _raw_stream(index: int, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(index)).cuda_stream
+
+
+def _like(name: str, t: torch.Tensor, shape, dtype, index: int):
+    """`t` is contiguous, of this shape and dtype, on CUDA device `index`."""
+    if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {tuple(shape)} {dtype} on cuda:{index} is needed, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int) -> torch.Tensor:
+    """An output of like's shape and dtype, contiguous: checked if given, else allocated."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _like(name, t, shape, dtype, dev)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _like(name, t, like.shape, like.dtype, index)
     return t
 
 
-def _on(dev: torch.device):
-    """Makes the tensors' device current for a call (launches and device queries go to the current device)."""
-    return torch.cuda.device(dev)
+def _f32(name: str, t: Optional[torch.Tensor], shape, like: torch.Tensor, index: int) -> torch.Tensor:
+    if t is None:
+        return like.new_empty(shape, dtype=torch.float32)
+    _like(name, t, shape, torch.float32, index)
+    return t
 
 
-def _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep) -> CrossAttnDesc:
-    for name, t in (("Q", Q), ("K", K), ("V", V)):
-        _heads_first(name, t)
-        if t.device != Q.device:
-            raise ValueError(f"{name} is on {t.device}, Q on {Q.device}")
+def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int):
+    """(tensor to keep until the launch, its address, its bytes)."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = like.new_empty((need,), dtype=torch.uint8)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{index} is needed")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _status(t: Optional[torch.Tensor], index: int):
+    if t is None:
+        return None
+    if t.get_device() != index or t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError(f"status: int32 on cuda:{index} is needed")
+    return t.data_ptr()
+
+
+def _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep) -> Tuple[int, CrossAttnDesc]:
+    index = _device_of(Q)
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError("Q, K and V are [rows, heads, channels]")
     nq, Hq, d = Q.shape
-    nkv, Hkv, _ = K.shape
-    if K.shape[2] != d or V.shape != K.shape:
+    nkv, Hkv, dk = kshape = K.shape
+    if dk != d or V.shape != kshape:
         raise ValueError(f"Q {tuple(Q.shape)}, K {tuple(K.shape)} and V {tuple(V.shape)} do not fit together")
-    G = q_off.numel() - 1
-    for name, t in (("q_off", q_off), ("kv_off", kv_off)):
-        _like(name, t, (max(G, 0) + 1,), torch.int32, Q.device)
+    strides = []
+    for name, t in (("Q", Q), ("K", K), ("V", V)):
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{name}: bf16 is needed, got {t.dtype}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, Q on {Q.device}")
+        row, head, one = t.stride()
+        if one != 1 and d > 1:
+            raise ValueError(f"{name}: contiguous channels are needed (rows and heads may be strided)")
+        strides += (row, head)
+    offs = q_off.shape
+    if q_off.dim() != 1 or offs[0] < 1:
+        raise ValueError("q_off: G + 1 offsets are needed")
+    _like("q_off", q_off, offs, torch.int32, index)
+    _like("kv_off", kv_off, offs, torch.int32, index)
     if kv_keep is not None:
         if kv_keep.dtype not in (torch.uint8, torch.bool):
             raise TypeError(f"kv_keep: uint8 or bool is needed, got {kv_keep.dtype}")
-        _like("kv_keep", kv_keep, (nkv,), kv_keep.dtype, Q.device)
-    return CrossAttnDesc(nq, nkv, Hq, Hkv, d, G, q_off.data_ptr(), kv_off.data_ptr(), int(max_q), int(max_kv),
-                         kv_keep.data_ptr() if kv_keep is not None else None,
-                         float(scale) if scale is not None else d ** -0.5, Q.stride(0), Q.stride(1), K.stride(0),
-                         K.stride(1), V.stride(0), V.stride(1))
-
-
-def _workspace(ws: Optional[torch.Tensor], need: int, dev) -> Tuple[Optional[torch.Tensor], int]:
-    if ws is None:
-        if not need:
-            return None, 0
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
-    _cuda(ws)
-    if ws.device != dev:
-        raise ValueError(f"workspace is on {ws.device}, the inputs on {dev}")
-    return ws, ws.numel() * ws.element_size()
+        _like("kv_keep", kv_keep, (nkv,), kv_keep.dtype, index)
+        kv_keep = kv_keep.data_ptr()
+    return index, CrossAttnDesc(nq, nkv, Hq, Hkv, d, offs[0] - 1, q_off.data_ptr(), kv_off.data_ptr(), min(int(max_q), nq),
+                                min(int(max_kv), nkv), kv_keep, d ** -0.5 if scale is None else float(scale), *strides)
 
 
 def svconv_cross_attn_fwd_workspace_size(desc: CrossAttnDesc) -> int:
@@ -473,15 +507,14 @@ def svconv_cross_attn_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_o
 
     scale defaults to 1 / sqrt(d); kv_keep [nkv] (uint8 or bool) leaves keys out.  Rows of no group
     are not written."""
-    desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
-    dev = Q.device
-    _cuda(status)
-    out = _ensure("out", out, Q.shape, torch.bfloat16, dev)
-    lse = _ensure("lse", lse, Q.shape[:2], torch.float32, dev)
-    with _on(dev):
-        workspace, ws_bytes = _workspace(workspace, svconv_cross_attn_fwd_workspace_size(desc), dev)
-        rc = lib().svconv_cross_attn_fwd(ctypes.byref(desc), _ptr(Q), _ptr(K), _ptr(V), _ptr(out), _ptr(lse),
-                                         _ptr(workspace), ws_bytes, _ptr(status), _stream(Q, stream))
+    index, desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
+    out = _same("out", out, Q, index)
+    lse = _f32("lse", lse, Q.shape[:2], Q, index)
+    L, ref = lib(), ctypes.byref(desc)
+    with _current(index):
+        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index)
+        rc = L.svconv_cross_attn_fwd(ref, Q.data_ptr(), K.data_ptr(), V.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                     ws_ptr, ws_bytes, _status(status, index), _raw_stream(index, stream))
     _check("svconv_cross_attn_fwd", rc)
     return out, lse
 
@@ -493,20 +526,17 @@ def svconv_cross_attn_bwd(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V:
                           dV: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                           status: Optional[torch.Tensor] = None, stream=None):
     """(dQ, dK, dV) of svconv_cross_attn_fwd from dO and the forward's O and lse; contiguous bf16."""
-    desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
-    dev = Q.device
-    _cuda(status)
-    _like("dO", dO, Q.shape, torch.bfloat16, dev)
-    _like("O", O, Q.shape, torch.bfloat16, dev)
-    _like("lse", lse, Q.shape[:2], torch.float32, dev)
-    dQ = _ensure("dQ", dQ, Q.shape, torch.bfloat16, dev)
-    dK = _ensure("dK", dK, K.shape, torch.bfloat16, dev)
-    dV = _ensure("dV", dV, V.shape, torch.bfloat16, dev)
-    with _on(dev):
-        workspace, ws_bytes = _workspace(workspace, svconv_cross_attn_bwd_workspace_size(desc), dev)
-        rc = lib().svconv_cross_attn_bwd(ctypes.byref(desc), _ptr(dO), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
-                                         _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace), ws_bytes, _ptr(status),
-                                         _stream(Q, stream))
+    index, desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
+    _like("dO", dO, Q.shape, torch.bfloat16, index)
+    _like("O", O, Q.shape, torch.bfloat16, index)
+    _like("lse", lse, Q.shape[:2], torch.float32, index)
+    dQ, dK, dV = _same("dQ", dQ, Q, index), _same("dK", dK, K, index), _same("dV", dV, V, index)
+    L, ref = lib(), ctypes.byref(desc)
+    with _current(index):
+        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index)
+        rc = L.svconv_cross_attn_bwd(ref, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+                                     lse.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws_ptr, ws_bytes,
+                                     _status(status, index), _raw_stream(index, stream))
     _check("svconv_cross_attn_bwd", rc)
     return dQ, dK, dV
 
@@ -516,35 +546,36 @@ _ROPE_LAYOUTS = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED, ROPE_HALF: 
 
 
 def _qk_common(Q, K, pq, pk, freq, layout, axis_pairs, wq, wk):
-    """Checked sides, the shared arguments of both directions."""
-    dev, dt, d = Q.device, _dtype_code(Q), Q.shape[-1]
-    if dt == E4M3:
-        raise TypeError("svconv_qk_norm_rope takes fp32 or bf16")
+    """Checked sides, and the arguments that both directions share."""
+    index, dtype = _device_of(Q), Q.dtype
+    code = F32 if dtype is torch.float32 else BF16 if dtype is torch.bfloat16 else None
+    if code is None:
+        raise TypeError(f"fp32 or bf16 is needed, got {dtype}")
     if layout not in _ROPE_LAYOUTS:
         raise ValueError(f"layout {layout!r}: 'half' or 'interleaved'")
-    _like("freq", freq, (freq.numel(),), torch.float64, dev)
+    pairs = freq.numel()
+    _like("freq", freq, (pairs,), torch.float64, index)
     axes = pq.shape[1] if pq.dim() == 2 else 1
-    split = [freq.numel()] if axis_pairs is None else [int(a) for a in axis_pairs]
-    if len(split) != axes or sum(split) != freq.numel():
-        raise ValueError(f"axis_pairs {split}: {axes} counts that add up to {freq.numel()} frequencies are needed")
+    split = (pairs,) if axis_pairs is None else axis_pairs
+    if len(split) != axes or not 1 <= axes <= 3 or sum(split) != pairs:
+        raise ValueError(f"axis_pairs {split}: {axes} counts that add up to {pairs} frequencies are needed, for at most 3 axes")
+    d = Q.shape[-1]
     sides = []
     for name, x, pos, w in (("Q", Q, pq, wq), ("K", K, pk, wk)):
-        if not x.is_cuda:
-            raise ValueError("svconv operates on CUDA tensors only")
-        if x.dim() != 3 or x.shape[2] != d or x.dtype != Q.dtype or x.device != dev:
-            raise ValueError(f"{name}: [rows, heads, {d}] {Q.dtype} on {dev} is needed")
+        if x.dim() != 3 or x.shape[2] != d or x.dtype is not dtype or x.get_device() != index:
+            raise ValueError(f"{name}: [rows, heads, {d}] {dtype} on cuda:{index} is needed")
         n, H, _ = x.shape
-        if x.numel() and ((d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d)):
+        row, head, one = x.stride()
+        if n and ((d > 1 and one != 1) or (H > 1 and head != d)):
             raise ValueError(f"{name}: contiguous heads are needed (rows may be strided)")
-        _like(f"positions of {name}", pos, (n, axes) if pos.dim() == 2 else (n,), torch.int32, dev)
-        if (pos.shape[1] if pos.dim() == 2 else 1) != axes:
+        if pos.dim() == 1 and axes != 1:
             raise ValueError("the positions of Q and K have different numbers of axes")
+        _like(f"positions of {name}", pos, (n, axes) if pos.dim() == 2 else (n,), torch.int32, index)
         if w is not None:
-            _like(f"weight of {name}", w, (d,), torch.float32, dev)
-        sides.append(QkSide(x.data_ptr(), x.stride(0) if n > 1 else H * d, n, H, pos.data_ptr(),
-                            w.data_ptr() if w is not None else None, None, None, None, None))
-    split_c = (ctypes.c_int32 * 3)(*split)
-    return dev, sides, (dt, d, 2 * freq.numel(), _ROPE_LAYOUTS[layout], _ptr(freq), axes, split_c)
+            _like(f"weight of {name}", w, (d,), torch.float32, index)
+            w = w.data_ptr()
+        sides.append(QkSide(x.data_ptr(), row if n > 1 else H * d, n, H, pos.data_ptr(), w))
+    return index, sides, (code, d, 2 * pairs, _ROPE_LAYOUTS[layout], freq.data_ptr(), axes, (ctypes.c_int32 * 3)(*split))
 
 
 def svconv_qk_norm_rope_fwd(Q: torch.Tensor, K: torch.Tensor, pos_q: torch.Tensor, pos_k: torch.Tensor,
@@ -556,12 +587,11 @@ def svconv_qk_norm_rope_fwd(Q: torch.Tensor, K: torch.Tensor, pos_q: torch.Tenso
     pos_* int32 [n] or [n, axes] (the (t, y, x) coords table serves as it is), freq fp64 [rot / 2] radians
     per unit of position (the first 2 * len(freq) channels are rotated), axis_pairs the number of pairs that
     follow each axis.  Yq / Yk may be Q / K themselves when those are contiguous."""
-    dev, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
-    Yq = _ensure("Yq", Yq, Q.shape, Q.dtype, dev)
-    Yk = _ensure("Yk", Yk, K.shape, K.dtype, dev)
+    index, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
+    Yq, Yk = _same("Yq", Yq, Q, index), _same("Yk", Yk, K, index)
     sq.y, sk.y = Yq.data_ptr(), Yk.data_ptr()
-    with _on(dev):
-        rc = lib().svconv_qk_norm_rope_fwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _stream(Q, stream))
+    with _current(index):
+        rc = lib().svconv_qk_norm_rope_fwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _raw_stream(index, stream))
     _check("svconv_qk_norm_rope_fwd", rc)
     return Yq, Yk
 
@@ -578,23 +608,27 @@ def svconv_qk_norm_rope_bwd(dYq: torch.Tensor, dYk: torch.Tensor, Q: torch.Tenso
                             dwk: Optional[torch.Tensor] = None, want_dw: bool = True,
                             workspace: Optional[torch.Tensor] = None, stream=None):
     """(dQ, dK, dwq, dwk) of svconv_qk_norm_rope_fwd (dwq, dwk fp32 [d], None unless want_dw)."""
-    dev, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
+    index, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
     d = Q.shape[2]
-    _like("dYq", dYq, Q.shape, Q.dtype, dev)
-    _like("dYk", dYk, K.shape, K.dtype, dev)
-    dQ = _ensure("dQ", dQ, Q.shape, Q.dtype, dev)
-    dK = _ensure("dK", dK, K.shape, K.dtype, dev)
+    _like("dYq", dYq, Q.shape, Q.dtype, index)
+    _like("dYk", dYk, K.shape, K.dtype, index)
+    dQ, dK = _same("dQ", dQ, Q, index), _same("dK", dK, K, index)
     if want_dw:
-        dwq = _ensure("dwq", dwq, (d,), torch.float32, dev)
-        dwk = _ensure("dwk", dwk, (d,), torch.float32, dev)
-    for s, dy, dx, dw in ((sq, dYq, dQ, dwq), (sk, dYk, dK, dwk)):
-        s.dy, s.dx, s.dw = dy.data_ptr(), dx.data_ptr(), dw.data_ptr() if dw is not None else None
-    with _on(dev):
-        workspace, ws_bytes = _workspace(workspace, svconv_qk_norm_rope_bwd_workspace_size(d), dev)
-        rc = lib().svconv_qk_norm_rope_bwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _ptr(workspace),
-                                           ws_bytes, _stream(Q, stream))
+        dwq, dwk = _f32("dwq", dwq, (d,), Q, index), _f32("dwk", dwk, (d,), Q, index)
+        sq.dw, sk.dw = dwq.data_ptr(), dwk.data_ptr()
+    else:
+        dwq = dwk = None
+    sq.dy, sq.dx, sk.dy, sk.dx = dYq.data_ptr(), dQ.data_ptr(), dYk.data_ptr(), dK.data_ptr()
+    L = lib()
+    with _current(index):
+        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_qk_norm_rope_bwd_workspace_size(d), Q, index)
+        rc = L.svconv_qk_norm_rope_bwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), ws_ptr, ws_bytes,
+                                       _raw_stream(index, stream))
     _check("svconv_qk_norm_rope_bwd", rc)
     return dQ, dK, dwq, dwk
+
+
+_GRAD_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
@@ -602,26 +636,34 @@ def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Op
                       stream=None) -> torch.Tensor:
     """Scale the gradients (fp32 or bf16, contiguous, one device) by min(1, max_norm / (norm + 1e-6)), in place
     or into `out`; returns their global norm (fp32 scalar tensor).  max_norm = inf takes the norm alone."""
+    T = torch.Tensor
     grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+    count = len(grads)
     if not grads and norm is None:
         raise ValueError("no gradients and no norm tensor: the device is unknown")
-    dev = grads[0].device if grads else norm.device
-    table = (Grad * max(len(grads), 1))()
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        _cuda(g, o)
-        if g.device != dev or o.device != dev or o.dtype != g.dtype or o.shape != g.shape:
-            raise ValueError(f"gradient {i}: one device, and outputs of the gradients' shapes and types are needed")
-        e = table[i]
-        e.src, e.dst, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g)
-    norm = _ensure("norm", norm, (), torch.float32, dev)
-    with _on(dev):
-        need = int(lib().svconv_clip_grads_workspace_size(table, len(grads)))
-        workspace, ws_bytes = _workspace(workspace, max(need, 16), dev)
-        rc = lib().svconv_clip_grads(table, len(grads), float(max_norm), _ptr(norm), _ptr(workspace), ws_bytes,
-                                     _stream(norm, stream))
+    index = _device_of(grads[0] if grads else norm)
+    dtypes = [g.dtype for g in grads]
+    if not set(dtypes) <= _GRAD_CODES.keys():
+        raise TypeError(f"fp32 or bf16 gradients are needed, got {set(dtypes)}")
+    every = grads
+    sizes = list(map(T.numel, grads))
+    src = dst = list(map(T.data_ptr, grads))
+    if out is not None:
+        outs = list(out)
+        if [o.dtype for o in outs] != dtypes or [o.shape for o in outs] != [g.shape for g in grads]:
+            raise ValueError("outputs of the gradients' shapes and types are needed")
+        every = grads + outs
+        dst = list(map(T.data_ptr, outs))
+    if any(i != index for i in map(T.get_device, every)) or not all(map(T.is_contiguous, every)):
+        raise ValueError(f"contiguous tensors on cuda:{index} are needed")
+    # svconv_grad records: src, dst, numel, dtype (the low word of the last 8 bytes)
+    flat = array.array("q", itertools.chain.from_iterable(zip(src, dst, sizes, map(_GRAD_CODES.get, dtypes))))
+    table = flat.buffer_info()[0] if count else None
+    norm = _f32("norm", norm, (), grads[0] if grads else norm, index)
+    L = lib()
+    with _current(index):
+        ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index)
+        rc = L.svconv_clip_grads(table, count, float(max_norm), norm.data_ptr(), ws_ptr, ws_bytes, _raw_stream(index, stream))
     _check("svconv_clip_grads", rc)
     return norm
 
