@@ -49,30 +49,56 @@ struct QkParams {
   float* part;                     // backward: [ctas][d] partial sums of dw
 };
 
-// A lane's 8 channels of a head as loaded, from channels a and b on, four each: bf16 in 4 words, fp32 in 8
+// Two fp32 values that one instruction handles together
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A lane's four pairs of a head: first members in a[0], a[1], second ones in b[0], b[1].
+struct Pairs {
+  f2 a[2], b[2];
+};
+
+// The same as loaded (bf16 in 4 words, fp32 in 8): for the half layout four channels from a and four from b on,
+// for the interleaved one the eight channels from a on.
 template <typename T>
 struct Raw {
   uint32_t v[sizeof(T) * 2];
 };
 
 template <typename T, bool HALF>
-__device__ __forceinline__ Raw<T> load8(const T* p, int a, int b) {
+__device__ __forceinline__ Raw<T> load8(const T* p, int b_off) {
   Raw<T> r;
   if constexpr (sizeof(T) == 4) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p + a)), w = __ldcs(reinterpret_cast<const uint4*>(p + b));
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p)), w = __ldcs(reinterpret_cast<const uint4*>(p + b_off));
     r.v[0] = u.x, r.v[1] = u.y, r.v[2] = u.z, r.v[3] = u.w, r.v[4] = w.x, r.v[5] = w.y, r.v[6] = w.z, r.v[7] = w.w;
   } else if constexpr (HALF) {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p + a)), w = __ldcs(reinterpret_cast<const uint2*>(p + b));
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p)), w = __ldcs(reinterpret_cast<const uint2*>(p + b_off));
     r.v[0] = u.x, r.v[1] = u.y, r.v[2] = w.x, r.v[3] = w.y;
   } else {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p + a));
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
     r.v[0] = u.x, r.v[1] = u.y, r.v[2] = u.z, r.v[3] = u.w;
   }
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void widen(const Raw<T>& r, float (&f)[8]) {
+template <typename T, bool HALF>
+__device__ __forceinline__ Pairs widen(const Raw<T>& r) {
+  float f[8];
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.v[i]);
@@ -83,154 +109,214 @@ __device__ __forceinline__ void widen(const Raw<T>& r, float (&f)[8]) {
       f[2 * i + 1] = __uint_as_float(r.v[i] & 0xffff0000u);
     }
   }
+  Pairs v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v.a[i] = HALF ? pack2(f[2 * i], f[2 * i + 1]) : pack2(f[4 * i], f[4 * i + 2]);
+    v.b[i] = HALF ? pack2(f[4 + 2 * i], f[5 + 2 * i]) : pack2(f[4 * i + 1], f[4 * i + 3]);
+  }
+  return v;
 }
 
 template <typename T, bool HALF>
-__device__ __forceinline__ void store8(T* p, int a, int b, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T* p, int b_off, const Pairs& v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    unpack2(v.a[i], f[HALF ? 2 * i : 4 * i], f[HALF ? 2 * i + 1 : 4 * i + 2]);
+    unpack2(v.b[i], f[HALF ? 4 + 2 * i : 4 * i + 1], f[HALF ? 5 + 2 * i : 4 * i + 3]);
+  }
   if constexpr (sizeof(T) == 4) {
-    __stcs(reinterpret_cast<float4*>(p + a), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4*>(p + b), make_float4(f[4], f[5], f[6], f[7]));
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p + b_off), make_float4(f[4], f[5], f[6], f[7]));
   } else {
-    uint32_t v[4];
+    uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+      u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     if constexpr (HALF) {
-      __stcs(reinterpret_cast<uint2*>(p + a), make_uint2(v[0], v[1]));
-      __stcs(reinterpret_cast<uint2*>(p + b), make_uint2(v[2], v[3]));
+      __stcs(reinterpret_cast<uint2*>(p), make_uint2(u[0], u[1]));
+      __stcs(reinterpret_cast<uint2*>(p + b_off), make_uint2(u[2], u[3]));
     } else {
-      __stcs(reinterpret_cast<uint4*>(p + a), make_uint4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
     }
   }
 }
 
+// Sum over the lanes of a head; LANES: known when compiling, or 0.
+template <int LANES>
 __device__ __forceinline__ float sum_lanes(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (LANES > 0) {
+#pragma unroll
+    for (int o = LANES >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  } else {
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  }
   return v;
 }
 
-// Turn (INVERSE: back) the lane's four pairs by the angles at cs / sn: channels i and 4 + i, or 2i and 2i + 1.
-template <bool HALF, bool INVERSE>
-__device__ __forceinline__ void rotate(float (&f)[8], const float* cs, const float* sn) {
-  const float4 c4 = *reinterpret_cast<const float4*>(cs), s4 = *reinterpret_cast<const float4*>(sn);
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+__device__ __forceinline__ float dot8(const Pairs& x, const Pairs& y) {
+  f2 s = mul2(x.a[0], y.a[0]);
+  s = fma2(x.a[1], y.a[1], s);
+  s = fma2(x.b[0], y.b[0], s);
+  s = fma2(x.b[1], y.b[1], s);
+  float lo, hi;
+  unpack2(s, lo, hi);
+  return lo + hi;
+}
+
+// Turn (INVERSE: back) the lane's four pairs by the angles at cs / sn.
+template <bool INVERSE>
+__device__ __forceinline__ void rotate(Pairs& v, const float* cs, const float* sn) {
+  const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cs), s = *reinterpret_cast<const ulonglong2*>(sn);
+  const f2 minus = pack2(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float& a = f[HALF ? i : 2 * i];
-    float& b = f[HALF ? 4 + i : 2 * i + 1];
-    const float z = INVERSE ? -s[i] : s[i];
-    const float t = a * c[i] - b * z;
-    b = a * z + b * c[i];
-    a = t;
+  for (int i = 0; i < 2; ++i) {
+    const f2 ci = i ? c.y : c.x, si = i ? s.y : s.x, ni = mul2(si, minus);
+    const f2 a = v.a[i];
+    v.a[i] = fma2(a, ci, mul2(v.b[i], INVERSE ? si : ni));
+    v.b[i] = fma2(v.b[i], ci, mul2(a, INVERSE ? ni : si));
+  }
+}
+
+// sine and cosine of pos times a frequency (a binary fraction of a turn per position)
+template <typename T>
+__device__ __forceinline__ void turn_by(unsigned long long f, int pos, float& s, float& c) {
+  const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
+  const uint32_t frac = hi * (uint32_t)pos + __umulhi(lo, (uint32_t)pos) - (pos < 0 ? lo : 0u);
+  if constexpr (sizeof(T) == 4) {
+    sincospif((float)(int)frac * 4.656612873077393e-10f, &s, &c);  // 2^-31: the angle over pi, -1 .. 1
+  } else {
+    const float x = (float)(int)frac * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    s = __sinf(x);
+    c = __cosf(x);
   }
 }
 
 // One warp's share of a side: TPB tokens of kQkBatch / TPB chunks each per step (TPB = 1: as many
-// steps per token as its chunks need).  dw gathers the lane's 8 channels of the weight gradient.
-template <typename T, bool HALF, bool BWD, int TPB>
-__device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& sd, int cta, const unsigned long long* turn, float* cs,
-                                          float* sn, float (&dw)[8]) {
+// steps per token as its chunks need).  dw gathers the lane's share of the weight gradient.
+template <typename T, bool HALF, bool BWD, int LANES, int TPB>
+__device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& side, int cta, const unsigned long long* turn, float* cs,
+                                          float* sn, Pairs& dw) {
   constexpr int CPB = kQkBatch / TPB;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (p.lanes - 1), hsub = lane / p.lanes, heads_per = 32 / p.lanes;
-  const bool on = sub * 8 < p.d, turned = sub * 4 < p.pairs;
-  const int a = HALF && turned ? sub * 4 : sub * 8, b = HALF && turned ? a + p.pairs : a + 4;
-  float w[8];
+  const int lanes = LANES > 0 ? LANES : p.lanes;
+  const int sub = lane & (lanes - 1), hsub = lane / lanes, heads_per = 32 / lanes;
+  const int n = side.n, H = side.H, d = p.d, pairs = p.pairs, axes = p.axes, chunks = side.chunks;
+  const bool on = sub * 8 < d, turned = sub * 4 < pairs;
+  const int a = on ? (HALF && turned ? sub * 4 : sub * 8) : 0, b_off = HALF && turned ? pairs : 4;
+  Pairs w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = on ? (sd.w ? sd.w[i < 4 ? a + i : b + i - 4] : 1.f) : 0.f;
-  const float inv_d = 1.f / (float)p.d;
-  const T* x = static_cast<const T*>(sd.x);
-  const T* dy = static_cast<const T*>(sd.dy);
-  T* out = static_cast<T*>(sd.out);
-  const int64_t step = (int64_t)sd.ctas * kQkWarps * TPB;
-  for (int64_t t0 = ((int64_t)cta * kQkWarps + warp) * TPB; t0 < sd.n; t0 += step) {
-    for (int ch0 = 0; ch0 < sd.chunks; ch0 += CPB) {
+  for (int i = 0; i < 2; ++i) {
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int at = 2 * i + k;
+      f[k] = side.w ? side.w[HALF ? a + at : a + 2 * at] : 1.f;
+      f[2 + k] = side.w ? side.w[HALF ? a + b_off + at : a + 2 * at + 1] : 1.f;
+    }
+    w.a[i] = pack2(f[0], f[1]);
+    w.b[i] = pack2(f[2], f[3]);
+  }
+  const float inv_d = 1.f / (float)d, eps = p.eps;
+  const int64_t x_row = side.x_row, row = (int64_t)H * d;
+  const int64_t first = (int64_t)(cta * kQkWarps + warp) * TPB, step = (int64_t)side.ctas * kQkWarps * TPB;
+  // lanes without a channel, a head or a token of their own load another's (in bounds) and store nothing
+  const T* x = static_cast<const T*>(side.x) + first * x_row + a;
+  const T* dy = BWD ? static_cast<const T*>(side.dy) + first * row + a : nullptr;
+  T* out = static_cast<T*>(side.out) + first * row + a;
+  const int32_t* pos = side.pos + first * axes;
+  const unsigned long long turn0 = lane < pairs ? turn[lane] : 0;
+  const int axis0 = lane < p.cut1 ? 0 : lane < p.cut2 ? 1 : 2;
+  for (int64_t t0 = first; t0 < n; t0 += step, x += step * x_row, out += step * row, pos += step * axes) {
+    const int last = (int)min((int64_t)TPB, n - t0) - 1;  // the last token of the step
+    for (int ch0 = 0; ch0 < chunks; ch0 += CPB) {
       Raw<T> rx[kQkBatch], rg[BWD ? kQkBatch : 1];
+      {
+        const T *px = x, *pg = dy;
 #pragma unroll
-      for (int u = 0; u < kQkBatch; ++u) {
-        const int64_t t = t0 + u / CPB;
-        const int h = (ch0 + u % CPB) * heads_per + hsub;
+        for (int u = 0; u < TPB; ++u) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) * 2; ++i) {
-          rx[u].v[i] = 0u;
-          if constexpr (BWD) rg[u].v[i] = 0u;
-        }
-        if (on && t < sd.n && h < sd.H) {
-          rx[u] = load8<T, HALF>(x + t * sd.x_row + h * p.d, a, b);
-          if constexpr (BWD) rg[u] = load8<T, HALF>(dy + (t * sd.H + h) * p.d, a, b);
+          for (int c = 0; c < CPB; ++c) {
+            const int at = min((ch0 + c) * heads_per + hsub, H - 1) * d;
+            rx[u * CPB + c] = load8<T, HALF>(px + at, b_off);
+            if constexpr (BWD) rg[u * CPB + c] = load8<T, HALF>(pg + at, b_off);
+          }
+          if (u < last) {
+            px += x_row;
+            if constexpr (BWD) pg += row;
+          }
         }
       }
       if (ch0 == 0) {
         __syncwarp();  // the previous step's readers are done
-        const int total = TPB * p.pairs;
-        for (int i = lane; i < total; i += 32) {
-          const int tt = TPB == 1 ? 0 : i / p.pairs, pr = TPB == 1 ? i : i - tt * p.pairs;
-          if (t0 + tt < sd.n) {
-            const int axis = pr < p.cut1 ? 0 : pr < p.cut2 ? 1 : 2;
-            const int pos = sd.pos[(t0 + tt) * p.axes + axis];
-            const unsigned long long f = turn[pr];
-            const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
-            const uint32_t frac = hi * (uint32_t)pos + __umulhi(lo, (uint32_t)pos) - (pos < 0 ? lo : 0u);
-            const float turns = (float)(int)frac * 2.3283064365386963e-10f;  // 2^-32: -1/2 .. 1/2
-            if constexpr (sizeof(T) == 4) {
-              sincospif(2.f * turns, &sn[i], &cs[i]);
-            } else {
-              sn[i] = __sinf(6.283185307179586f * turns);
-              cs[i] = __cosf(6.283185307179586f * turns);
-            }
-          }
+        const int32_t* pp = pos;
+#pragma unroll
+        for (int u = 0; u < TPB; ++u) {
+          if (lane < pairs) turn_by<T>(turn0, pp[axis0], sn[u * pairs + lane], cs[u * pairs + lane]);
+          for (int i = lane + 32; i < pairs; i += 32)
+            turn_by<T>(turn[i], pp[i < p.cut1 ? 0 : i < p.cut2 ? 1 : 2], sn[u * pairs + i], cs[u * pairs + i]);
+          if (u < last) pp += axes;
         }
         __syncwarp();
       }
+      T* po = out;
 #pragma unroll
-      for (int u = 0; u < kQkBatch; ++u) {
-        const int64_t t = t0 + u / CPB;
-        const int h = (ch0 + u % CPB) * heads_per + hsub;
-        if (t >= sd.n || ch0 + u % CPB >= sd.chunks) continue;  // uniform over the warp
-        const bool ok = on && h < sd.H;
-        float f[8];
-        widen(rx[u], f);
-        float ss = 0.f;
+      for (int u = 0; u < TPB; ++u) {
+        if (u > last) break;  // uniform over the warp
+        const float* tcs = cs + u * pairs + sub * 4;
+        const float* tsn = sn + u * pairs + sub * 4;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        const float rstd = rsqrtf(sum_lanes(ss, p.lanes) * inv_d + p.eps);
-        const float* tcs = cs + (u / CPB) * p.pairs + sub * 4;
-        const float* tsn = sn + (u / CPB) * p.pairs + sub * 4;
-        if constexpr (!BWD) {
+        for (int c = 0; c < CPB; ++c) {
+          if (CPB > 1 && ch0 + c >= chunks) break;  // uniform over the warp
+          const int h = (ch0 + c) * heads_per + hsub;
+          const bool ok = on && h < H;
+          Pairs f = widen<T, HALF>(rx[u * CPB + c]);
+          const float ss = dot8(f, f);
+          const float rstd = rsqrtf(fmaf(sum_lanes<LANES>(LANES > 0 || on ? ss : 0.f, lanes), inv_d, eps));
+          const f2 r2 = pack2(rstd, rstd);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * w[i];
-          if (turned) rotate<HALF, false>(f, tcs, tsn);
-          if (ok) store8<T, HALF>(out + (t * sd.H + h) * p.d, a, b, f);
-        } else {
-          float g[8];
-          widen(rg[u], g);
-          if (turned) rotate<HALF, true>(g, tcs, tsn);
-          float dot = 0.f;
+          for (int i = 0; i < 2; ++i) f.a[i] = mul2(f.a[i], r2), f.b[i] = mul2(f.b[i], r2);  // the normalised channels
+          if constexpr (!BWD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            f[i] *= rstd;  // the normalised channel
-            if (ok) dw[i] = fmaf(g[i], f[i], dw[i]);
-            g[i] *= w[i];
-            dot = fmaf(g[i], f[i], dot);
+            for (int i = 0; i < 2; ++i) f.a[i] = mul2(f.a[i], w.a[i]), f.b[i] = mul2(f.b[i], w.b[i]);
+            if (turned) rotate<false>(f, tcs, tsn);
+            if (ok) store8<T, HALF>(po + h * d, b_off, f);
+          } else {
+            Pairs g = widen<T, HALF>(rg[u * CPB + c]);
+            if (turned) rotate<true>(g, tcs, tsn);
+            if (ok) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) dw.a[i] = fma2(g.a[i], f.a[i], dw.a[i]), dw.b[i] = fma2(g.b[i], f.b[i], dw.b[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) g.a[i] = mul2(g.a[i], w.a[i]), g.b[i] = mul2(g.b[i], w.b[i]);
+            const float dot = dot8(g, f);
+            const float m = -sum_lanes<LANES>(LANES > 0 || on ? dot : 0.f, lanes) * inv_d;
+            const f2 m2 = pack2(m, m);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              g.a[i] = mul2(r2, fma2(f.a[i], m2, g.a[i]));
+              g.b[i] = mul2(r2, fma2(f.b[i], m2, g.b[i]));
+            }
+            if (ok) store8<T, HALF>(po + h * d, b_off, g);
           }
-          dot = sum_lanes(dot, p.lanes) * inv_d;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = rstd * (g[i] - f[i] * dot);
-          if (ok) store8<T, HALF>(out + (t * sd.H + h) * p.d, a, b, g);
         }
+        po += row;
       }
     }
+    if constexpr (BWD) dy += step * row;
   }
 }
 
 // CTAs resident on an SM: as many as the registers of a variant allow without spills.
 template <typename T, bool BWD>
-constexpr int kQkPerSm = BWD ? (sizeof(T) == 4 ? 2 : 3) : (sizeof(T) == 4 ? 3 : 4);
+constexpr int kQkPerSm = BWD && sizeof(T) == 4 ? 2 : 3;
 
 // CTAs 0 .. side[0].ctas-1 take the queries, the rest the keys; a side's warps stride over its tokens.
-template <typename T, bool HALF, bool BWD>
+template <typename T, bool HALF, bool BWD, int LANES>
 __global__ void __launch_bounds__(kQkWarps * 32, kQkPerSm<T, BWD>) qk_kernel(const __grid_constant__ QkParams p) {
   __shared__ __align__(16) float s_cs[kQkWarps][kQkBatch * kQkMaxPairs];
   __shared__ __align__(16) float s_sn[kQkWarps][kQkBatch * kQkMaxPairs];
@@ -246,24 +332,23 @@ __global__ void __launch_bounds__(kQkWarps * 32, kQkPerSm<T, BWD>) qk_kernel(con
   const bool is_k = (int)blockIdx.x >= p.side[0].ctas;
   const QkSide& sd = p.side[is_k ? 1 : 0];
   const int cta = (int)blockIdx.x - (is_k ? p.side[0].ctas : 0);
-  float dw[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+  Pairs dw = {{0ull, 0ull}, {0ull, 0ull}};
   if (sd.chunks == 1)
-    qk_tokens<T, HALF, BWD, 4>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, LANES, 4>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   else if (sd.chunks == 2)
-    qk_tokens<T, HALF, BWD, 2>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, LANES, 2>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   else
-    qk_tokens<T, HALF, BWD, 1>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
+    qk_tokens<T, HALF, BWD, LANES, 1>(p, sd, cta, s_turn, s_cs[warp], s_sn[warp], dw);
   if constexpr (BWD) {
     // dw of this CTA: warps and head slots in a fixed order
     __shared__ float s_dw[kQkWarps][32][8];
+    float* mine = s_dw[warp][threadIdx.x & 31];  // first members, then second ones
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_dw[warp][threadIdx.x & 31][i] = dw[i];
+    for (int i = 0; i < 2; ++i) unpack2(dw.a[i], mine[2 * i], mine[2 * i + 1]), unpack2(dw.b[i], mine[4 + 2 * i], mine[5 + 2 * i]);
     __syncthreads();
     for (int c = threadIdx.x; c < p.d; c += kQkWarps * 32) {
       // the lane and place that held channel c
-      int sub = c / 8, at = c % 8;
+      int sub = c / 8, at = HALF ? c % 8 : c % 8 / 2 + c % 2 * 4;
       if (HALF && c < 2 * p.pairs) {
         const int m = c < p.pairs ? c : c - p.pairs;
         sub = m / 4, at = m % 4 + (c < p.pairs ? 0 : 4);
@@ -326,7 +411,12 @@ cudaError_t launch_qk(QkParams& p, cudaStream_t s) {
   static_assert(kQkSms * kQkPerSm<T, BWD> <= kQkCtas, "the partial sums have kQkCtas slots");
   split_ctas(p, kQkSms * kQkPerSm<T, BWD>);
   const int grid = p.side[0].ctas + p.side[1].ctas;
-  return grid == 0 ? cudaSuccess : launch_pdl(qk_kernel<T, HALF, BWD>, dim3(grid), dim3(kQkWarps * 32), 0, s, p);
+  if (grid == 0) return cudaSuccess;
+  const dim3 g(grid), b(kQkWarps * 32);
+  // 64 and 128 channels (whole lane groups of a known size) have loops without a runtime bound
+  if (p.d == 64) return launch_pdl(qk_kernel<T, HALF, BWD, 8>, g, b, 0, s, p);
+  if (p.d == 128) return launch_pdl(qk_kernel<T, HALF, BWD, 16>, g, b, 0, s, p);
+  return launch_pdl(qk_kernel<T, HALF, BWD, 0>, g, b, 0, s, p);
 }
 
 int check_side(const svconv_qk_side& s, int dtype, int d, bool bwd) {

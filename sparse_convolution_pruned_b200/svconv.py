@@ -650,8 +650,8 @@ def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Op
     src = dst = list(map(T.data_ptr, grads))
     if out is not None:
         outs = list(out)
-        if [o.dtype for o in outs] != dtypes or [o.shape for o in outs] != [g.shape for g in grads]:
-            raise ValueError("outputs of the gradients' shapes and types are needed")
+        if [o.dtype for o in outs] != dtypes or list(map(T.numel, outs)) != sizes:
+            raise ValueError("outputs of the gradients' sizes and types are needed")
         every = grads + outs
         dst = list(map(T.data_ptr, outs))
     if any(i != index for i in map(T.get_device, every)) or not all(map(T.is_contiguous, every)):
