@@ -36,8 +36,9 @@ __device__ __forceinline__ int group_range(const int32_t* off, int g, int n, int
 constexpr int kTile = 128;             // query rows (query tokens x their r heads) and keys of a tile
 constexpr int kBlockBytes = kTile * 128;  // 128 rows of 64 bf16 channels, 128-byte swizzled
 constexpr int kSoftWarps = 8;          // two softmax warpgroups, one per stream
-constexpr int kFwdThreads = (kSoftWarps + 2) * 32;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kCheckWarp = kSoftWarps + 2;  // zeroes rows that take no part, ahead of the products
+constexpr int kThreads = (kSoftWarps + 3) * 32;
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
   asm volatile(
@@ -53,16 +54,78 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 values that one instruction handles together
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 pack2(uint32_t lo, uint32_t hi) { return pack2(__uint_as_float(lo), __uint_as_float(hi)); }
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The whole warp waits: lane 0 polls, the verdict is broadcast (control flow stays warp-uniform).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, err, kDefaultTimeoutNs);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+// Bounded waits.  The waits between products and softmax follow each other every few hundred cycles:
+// every thread polls, without a sleep hint (a thread put to sleep wakes late), in a loop of three instructions, and
+// nothing branches on the outcome: a call, a result to carry through the loops or one polling lane with a
+// broadcast each cost 10 to 25% of the kernels.  A wait that runs out raises the abort flag, after which every wait
+// returns at once and the loops run to their ends on whatever is there (in bounds; the status word tells).
+__device__ __forceinline__ uint32_t try_wait_many(uint64_t* bar, uint32_t parity) {
+  uint32_t left;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mov.u32 %0, 256;\n\t"
+      "ATTN_WAIT:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra ATTN_DONE;\n\t"
+      "sub.u32 %0, %0, 1;\n\t"
+      "setp.ne.u32 q, %0, 0;\n\t"
+      "@q bra ATTN_WAIT;\n\t"
+      "ATTN_DONE:\n\t}"
+      : "=&r"(left)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return left;
+}
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  if (try_wait_many(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!*abort_flag && !try_wait_many(bar, parity)) {
+    if (globaltimer_ns() - t0 > kDefaultTimeoutNs) {
+      *abort_flag = 1;
+      atomicOr(err, SVCONV_STATUS_TIMEOUT);
+    }
+  }
+}
+// The whole warp waits, and is converged afterwards.
+__device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  wait_for(bar, parity, abort_flag, err);
+  __syncwarp();
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -141,7 +204,8 @@ struct FwdParams {
 };
 
 struct FwdBarriers {
-  uint64_t qfull, kvfull[12], kvempty[12], sfull[2], pfull[2], odone[2], fin;
+  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], pfull[2], odone[2], fin;
+  uint32_t kept[10][4];  // keys that take part, of the tile whose V lies in this slot
   uint32_t tmem;
   int abort_flag;
 };
@@ -158,7 +222,7 @@ struct FwdShape {
 };
 
 template <int DB>
-__global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Sh = FwdShape<DB>;
   constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -179,7 +243,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->qfull, 1);
-    for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4), mbar_init(&bar->odone[s], 1);
     mbar_init(&bar->fin, 1);
     bar->abort_flag = 0;
@@ -210,6 +274,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
   // tiles of stream s, and the tile of its step i (counted from t_lo)
   auto steps_of = [&](int s) { return p.pair ? (tok0 + s * p.tokens < q1 ? nt : 0) : (nt + 1 - s) / 2; };
   auto tile_of = [&](int s, int i) { return p.pair ? i : 2 * i + s; };
+  auto masked = [&](int tile) { return p.keep || k0 + (t_lo + tile + 1) * kTile > k1; };
 
   int loaded = 0;  // K / V tiles whose loads were issued (the loader's count)
   if (warp == kLoadWarp) {
@@ -222,7 +287,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           tma_load_4d(sq + s * Sh::kTileBytes + b * kBlockBytes, &p.tq, &bar->qfull, b * 64, 0, hk, tok0 + s * p.tokens);
       for (; loaded < 2 * nt; ++loaded) {  // K, V of each tile in turn
         const int slot = loaded % NS;
-        if (loaded >= NS && !mbar_wait(&bar->kvempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err, kDefaultTimeoutNs)) break;
+        if (loaded >= NS) wait_for(&bar->kvempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+        if (*abort_flag) break;
         mbar_arrive_expect_tx(&bar->kvfull[slot], Sh::kTileBytes);
         for (int b = 0; b < DB; ++b)
           tma_load_3d(skv + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.tv : &p.tk, &bar->kvfull[slot], b * 64, hk,
@@ -235,25 +301,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, 0, 0), idesc_o = idesc_bf16_f32(kTile, dn, 0, 1);
       int k_seen = -1, v_seen = -1;  // newest K / V tile known to have landed
       auto seen = [&](int& newest, int tile, int which) {
-        if (tile <= newest) return true;
-        const int n = 2 * tile + which;
-        if (!warp_wait(&bar->kvfull[n % NS], (n / NS) & 1, abort_flag, err)) return false;
+        if (tile <= newest) return;
         newest = tile;
-        if (which) {  // rows of V behind the group's end or dropped by the mask must be zero: their weights are
-          const int j0 = k0 + (t_lo + tile) * kTile;
-          if (p.keep || j0 + kTile > k1) {
-            uint32_t w[4];
-            kept_words(p.keep, j0, k1, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ~w[i];
-            scrub_rows(skv + (n % NS) * Sh::kTileBytes, DB, kBlockBytes, w);
-          }
-        }
-        return true;
+        const int n = 2 * tile + which;
+        // rows of V behind the group's end or dropped by the mask must be zero: their weights are
+        wait_warp(which && masked(tile) ? &bar->vready[n % NS] : &bar->kvfull[n % NS], (n / NS) & 1, abort_flag, err);
       };
       auto issue_s = [&](int s, int i) {
         const int tile = tile_of(s, i);
-        if (!seen(k_seen, tile, 0)) return false;
+        seen(k_seen, tile, 0);
         if (lane == 0) {
           tc_fence_after();
           const uint64_t a0 = smem_desc_sw128(sq + (p.pair ? s : 0) * Sh::kTileBytes, 16, 1024);
@@ -267,11 +323,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           if (!p.pair || s == 1 || steps_of(1) == 0) tc_commit(&bar->kvempty[2 * tile % NS]);
         }
         __syncwarp();
-        return true;
       };
       auto issue_o = [&](int s, int i) {
         const int tile = tile_of(s, i);
-        if (!seen(v_seen, tile, 1)) return false;
+        seen(v_seen, tile, 1);
         if (lane == 0) {
           tc_fence_after();
           const int slot = (2 * tile + 1) % NS;
@@ -283,25 +338,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           if (!p.pair || s == 1 || steps_of(1) == 0) tc_commit(&bar->kvempty[slot]);
         }
         __syncwarp();
-        return true;
       };
-      bool ok = warp_wait(&bar->qfull, 0, abort_flag, err);
-      for (int s = 0; s < 2 && ok; ++s)
-        if (steps_of(s) > 0) ok = issue_s(s, 0);
+      wait_warp(&bar->qfull, 0, abort_flag, err);
+      for (int s = 0; s < 2; ++s)
+        if (steps_of(s) > 0) issue_s(s, 0);
       const int steps = steps_of(0);
-      for (int i = 0; i < steps && ok; ++i)
-        for (int s = 0; s < 2 && ok; ++s) {
+      for (int i = 0; i < steps; ++i)
+        for (int s = 0; s < 2; ++s) {
           if (i >= steps_of(s)) continue;
-          ok = warp_wait(&bar->pfull[s], i & 1, abort_flag, err);
+          wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
           const bool more = i + 1 < steps_of(s);
           if constexpr (DB == 1) {
-            if (ok && more) ok = issue_s(s, i + 1);
-            if (ok) ok = issue_o(s, i);
+            if (more) issue_s(s, i + 1);
+            issue_o(s, i);
           } else {
-            if (ok) ok = issue_o(s, i);
-            if (ok && more) {
-              ok = warp_wait(&bar->odone[s], i & 1, abort_flag, err);  // P shares S's columns
-              if (ok) ok = issue_s(s, i + 1);
+            issue_o(s, i);
+            if (more) {
+              wait_warp(&bar->odone[s], i & 1, abort_flag, err);  // P shares S's columns
+              issue_s(s, i + 1);
             }
           }
         }
@@ -311,6 +365,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         mbar_wait(&bar->fin, 0, &never, err, kDefaultTimeoutNs);
       }
       __syncwarp();
+    }
+  } else if (warp == kCheckWarp) {
+    for (int tile = 0; tile < nt; ++tile) {
+      const int n = 2 * tile + 1, slot = n % NS;
+      wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
+      if (masked(tile)) {
+        uint32_t w[4];
+        kept_words(p.keep, k0 + (t_lo + tile) * kTile, k1, w);
+        if (lane < 4) bar->kept[slot][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ~w[i];
+        scrub_rows(skv + slot * Sh::kTileBytes, DB, kBlockBytes, w);
+      }
+      warp_arrive(&bar->vready[slot]);
     }
   } else {
     // ------------------------------------------------------------ softmax: one thread per row
@@ -322,13 +390,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     const int steps = steps_of(s);
     const float ca = fmaxf(fabsf(p.c), 1e-30f);  // never 0: a masked score stays -inf when scaled
     float m = -INFINITY, l = 0.f;  // running maximum (of the raw scores, negated for a negative scale) and sum
-    bool ok = true;
     for (int i = 0; i < steps; ++i) {
-      const int j0 = k0 + (t_lo + tile_of(s, i)) * kTile;
-      const bool masked = p.keep || j0 + kTile > k1;
-      uint32_t kept[4];
-      if (masked) kept_words(p.keep, j0, k1, kept);
-      if (!(ok = warp_wait(&bar->sfull[s], i & 1, abort_flag, err))) break;
+      const int tile = tile_of(s, i);
+      const bool some = masked(tile);
+      wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
       tc_fence_after();
       if (warp_on) {
         uint32_t v[4][32];
@@ -341,19 +406,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[b][k] ^= 0x80000000u;
         }
-        if (masked) {
+        if (some) {
+          const int n = 2 * tile + 1;
+          wait_warp(&bar->vready[n % NS], (n / NS) & 1, abort_flag, err);
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t w = bar->kept[n % NS][b];
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (!(kept[b] >> k & 1u)) v[b][k] = 0xff800000u;
+              if (!(w >> k & 1u)) v[b][k] = 0xff800000u;
+          }
         }
         float mx[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          mx[b] = __uint_as_float(v[b][0]);
+          mx[b] = fmaxf(__uint_as_float(v[b][0]), __uint_as_float(v[b][1]));
 #pragma unroll
-          for (int k = 1; k < 32; ++k) mx[b] = fmaxf(mx[b], __uint_as_float(v[b][k]));
+          for (int k = 2; k < 32; k += 2) mx[b] = max3(mx[b], __uint_as_float(v[b][k]), __uint_as_float(v[b][k + 1]));
         }
         const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // a row that has seen no key yet takes the tile's maximum; later ones only a clear rise
@@ -361,12 +430,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         if (m == -INFINITY || (tile_max - m) * ca > kRescaleLog2) m = fmaxf(m, tile_max);
         const float mm = m == -INFINITY ? 0.f : m * ca;
         if (i > 0) {
-          ok = warp_wait(&bar->odone[s], (i - 1) & 1, abort_flag, err);
-          if (!ok) break;
+          wait_warp(&bar->odone[s], (i - 1) & 1, abort_flag, err);
           tc_fence_after();
-          const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
-          l *= a;
-          if (__any_sync(0xffffffffu, m != m_old && m_old != -INFINITY)) {
+          if (__any_sync(0xffffffffu, m != m_old)) {
+            const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
+            l *= a;
             for (int b = 0; b < 4 * DB; ++b) {
               uint32_t o[16];
               tmem_ld_x16(tmem + lanes + Sh::kO(s) + b * 16, o);
@@ -377,27 +445,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             }
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const f2 c2 = pack2(ca, ca), m2 = pack2(-mm, -mm);
+        f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float x = ex2(fmaf(__uint_as_float(v[2 * h + k / 16][2 * (k & 15)]), ca, -mm));
-            const float y = ex2(fmaf(__uint_as_float(v[2 * h + k / 16][2 * (k & 15) + 1]), ca, -mm));
-            sum[k & 3] += x + y;
+          for (int k = 0; k < 16; ++k) {
+            float x, y;
+            unpack2(fma2(pack2(v[h][2 * k], v[h][2 * k + 1]), c2, m2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[k & 3] = add2(sum[k & 3], pack2(x, y));
             w[k] = pack_bf16(x, y);
           }
-          tmem_st_32x32b_x32(tmem + lanes + Sh::kP(s) + h * 32, w);
+          tmem_st_x16(tmem + lanes + Sh::kP(s) + h * 16, w);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float x, y;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+        l += x + y;
         tmem_st_wait();
       }
       tc_fence_before();
       warp_arrive(&bar->pfull[s]);
     }
-    if (ok && steps > 0) {
-      ok = warp_wait(&bar->odone[s], (steps - 1) & 1, abort_flag, err);
+    if (steps > 0) {
+      wait_warp(&bar->odone[s], (steps - 1) & 1, abort_flag, err);
       tc_fence_after();
     }
     float m2 = l > 0.f ? m * ca : -INFINITY;  // the maximum in base 2; -inf: no key
@@ -408,7 +481,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     if (merge) {
       // both streams' last products, and with them every load into the ring, are done before it is reused
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (s == 1 && warp_on && ok) {
+      if (s == 1 && warp_on) {
         so[kCols * kTile + row] = m2;
         so[(kCols + 1) * kTile + row] = l;
 #pragma unroll
@@ -423,7 +496,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
     const bool writer = p.pair || s == 0;
-    if (warp_on && ok && writer) {
+    if (warp_on && writer) {
       float f0 = 1.f, f1 = 0.f;
       if (merge) {
         const float m1 = so[kCols * kTile + row], l1 = so[(kCols + 1) * kTile + row];
@@ -552,7 +625,8 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant
 // per tile where one pass with atomics on dQ would take 5.
 constexpr int kMove = 64;                  // rows of a moving tile
 constexpr int kMoveBlock = kMove * 128;    // bytes of its 64-channel block
-constexpr int kStatBytes = 544;            // lse and D of 64 rows (8 bytes each) from a 16-byte boundary on
+constexpr int kStat = 2 * kMove;           // a tile's statistics: -lse in base 2 of its 64 rows, then -D
+constexpr int kStatBytes = kStat * 4;
 
 struct BwdParams {
   CUtensorMap fq, fdo, fk, fv;   // boxes of the fixed tiles
@@ -563,14 +637,16 @@ struct BwdParams {
   int qblocks, qsplits, kblocks, ksplits;
   int q_items;                   // CTAs of the query pass (they come first)
   float c, scale;
-  const float2* stat;            // [Hkv][nq * r]: lse in base 2 (+inf for a row without keys), D
+  const float* stat;             // [Hkv][stat_tiles][kStat], see attn_stat_kernel
+  int stat_tiles;
   __nv_bfloat16 *dQ, *dK, *dV;
   float *part_q, *part_k, *part_v;  // [splits][rows][d] where a pass is split
   int* status;
 };
 
 struct BwdBarriers {
-  uint64_t ffull, mfull[8], mempty[8], sfull[2], pfull[2], pdone[2], adone[2], fin;
+  uint64_t ffull, mfull[8], mempty[8], mready[8], sfull[2], pfull[2], pdone[2], adone[2], fin;
+  uint32_t kept[8][2];  // query pass: keys of the slot's tile that take part
   uint32_t tmem;
   int abort_flag;
 };
@@ -646,8 +722,8 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       w[i] = __ballot_sync(0xffffffffu, on);
     }
   };
-  // first entry of the tile's statistics; the copy starts at the even entry before it
-  auto stat_of = [&](int t) { return (int64_t)hk * p.nq * p.r + (int64_t)(m0 + t * mtok) * p.r; };
+  // the statistics of query tile t of the group
+  auto stat_of = [&](int t) { return p.stat + ((int64_t)hk * p.stat_tiles + q0 / mtok + g + t) * kStat; };
 
   int loaded = 0;
   if (warp == kLoadWarp) {
@@ -664,8 +740,9 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
         }
       for (; loaded < nt; ++loaded) {
         const int slot = loaded % NS;
-        if (loaded >= NS && !mbar_wait(&bar->mempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err, kDefaultTimeoutNs)) break;
-        mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * m_bytes + (KEYS ? 528u : 0u));
+        if (loaded >= NS) wait_for(&bar->mempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+        if (*abort_flag) break;
+        mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * m_bytes + (KEYS ? (uint32_t)kStatBytes : 0u));
         for (int o = 0; o < 2; ++o)
           for (int b = 0; b < DB; ++b) {
             const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
@@ -673,14 +750,14 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
             else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
           }
         if constexpr (KEYS)
-          bulk_copy_g2s(sstat + slot * kStatBytes, p.stat + (stat_of(loaded) & ~(int64_t)1), 528u, &bar->mfull[slot]);
+          bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
       }
     }
   } else if (warp == kMmaWarp) {
     if (nt > 0) {
       const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
       const uint32_t idesc_s = idesc_bf16_f32(kTile, kMove, 0, 0), idesc_a = idesc_bf16_f32(kTile, dn, 0, 1);
-      bool ok = warp_wait(&bar->ffull, 0, abort_flag, err);
+      wait_warp(&bar->ffull, 0, abort_flag, err);
       // operand o of the scores of tile t into column col
       auto scores = [&](int o, int t, int col) {
         const uint64_t a0 = smem_desc_sw128(sf + o * Sh::kFixedBytes, 16, 1024);
@@ -696,32 +773,24 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
         for (int k = 0; k < kMove / 16; ++k)
           tc_mma_bf16_ts(tmem + acc, tmem + a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_a, (t | k) ? 1u : 0u);
       };
-      auto landed = [&](int t) {  // the tile is there, rows that take no part zeroed (they meet zero weights)
-        if (!warp_wait(&bar->mfull[t % NS], (t / NS) & 1, abort_flag, err)) return false;
-        if (partial(t)) {
-          uint32_t w[2];
-          kept(t, w);
-          w[0] = ~w[0], w[1] = ~w[1];
-          scrub_rows(sm + (t % NS) * Sh::kStageBytes, 2 * DB, kMoveBlock, w);
-        }
-        if (lane == 0) tc_fence_after();
-        return true;
+      auto landed = [&](int t) {  // rows that take no part are zero by then: they meet zero weights
+        wait_warp(partial(t) ? &bar->mready[t % NS] : &bar->mfull[t % NS], (t / NS) & 1, abort_flag, err);
+        tc_fence_after();
       };
-      for (int s = 0; s < 2 && ok; ++s)
+      for (int s = 0; s < 2; ++s)
         if (steps_of(s) > 0) {
-          ok = landed(s);
-          if (ok && lane == 0) {
+          landed(s);
+          if (lane == 0) {
             scores(0, s, Tm::S(s));
             scores(1, s, Tm::dP(s));
             tc_commit(&bar->sfull[s]);
           }
           __syncwarp();
         }
-      for (int t = 0; t < nt && ok; ++t) {
+      for (int t = 0; t < nt; ++t) {
         const int s = t & 1, ph = (t >> 1) & 1, next = t + 2;
-        ok = warp_wait(&bar->pfull[s], ph, abort_flag, err);
-        if (!ok) break;
-        if (next < nt && !(ok = landed(next))) break;
+        wait_warp(&bar->pfull[s], ph, abort_flag, err);
+        if (next < nt) landed(next);
         if (lane == 0) {
           tc_fence_after();
           if constexpr (Tm::kShared) {
@@ -733,11 +802,11 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
             tc_commit(&bar->adone[s]);
             tc_commit(&bar->mempty[t % NS]);
             if (next < nt) {
-              ok = mbar_wait(&bar->pdone[s], ph, abort_flag, err, kDefaultTimeoutNs);
-              if (ok) scores(0, next, Tm::S(s));
-              if (ok) ok = mbar_wait(&bar->adone[s], ph, abort_flag, err, kDefaultTimeoutNs);
-              if (ok) scores(1, next, Tm::dP(s));
-              if (ok) tc_commit(&bar->sfull[s]);
+              wait_for(&bar->pdone[s], ph, abort_flag, err);
+              scores(0, next, Tm::S(s));
+              wait_for(&bar->adone[s], ph, abort_flag, err);
+              scores(1, next, Tm::dP(s));
+              tc_commit(&bar->sfull[s]);
             }
           } else {
             if (next < nt) {
@@ -751,7 +820,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
             tc_commit(&bar->mempty[t % NS]);
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        __syncwarp();
       }
       if (lane == 0) {  // every issued product is complete before tensor memory is released
         tc_commit(&bar->fin);
@@ -760,62 +829,79 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       }
       __syncwarp();
     }
+  } else if (warp == kCheckWarp) {
+    for (int t = 0; t < nt; ++t) {
+      const int slot = t % NS;
+      wait_warp(&bar->mfull[slot], (t / NS) & 1, abort_flag, err);
+      if (partial(t)) {
+        uint32_t w[2];
+        kept(t, w);
+        if (lane < 2) bar->kept[slot][lane] = lane == 0 ? w[0] : w[1];
+        w[0] = ~w[0], w[1] = ~w[1];
+        scrub_rows(sm + slot * Sh::kStageBytes, 2 * DB, kMoveBlock, w);
+      }
+      warp_arrive(&bar->mready[slot]);
+    }
   } else {
     // ------------------------------------------------------------ P and dS: one thread per fixed row
     const int s = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const bool warp_on = (warp & 3) * 32 < left, row_on = row < left;
     const int steps = steps_of(s);
-    float row_lse = INFINITY, row_d = 0.f;
+    const f2 c2 = pack2(p.c, p.c);
+    f2 row_lse = pack2(-INFINITY, -INFINITY), row_d = 0ull;
     if (!KEYS && row_on) {
-      const float2 st = p.stat[(int64_t)hk * p.nq * p.r + (int64_t)f0 * p.r + row];
-      row_lse = st.x, row_d = st.y;
+      const int token = f0 - q0 + row / p.r;
+      const float* st = stat_of(token / mtok) + (token % mtok) * p.r + row % p.r;
+      row_lse = pack2(st[0], st[0]);
+      row_d = pack2(st[kMove], st[kMove]);
     }
-    bool ok = true;
     for (int i = 0; i < steps; ++i) {
       const int t = 2 * i + s;
-      uint32_t w[2] = {~0u, ~0u};
-      const bool some = partial(t);
-      if (some) kept(t, w);
-      if (KEYS && !(ok = warp_wait(&bar->mfull[t % NS], (t / NS) & 1, abort_flag, err))) break;
-      if (!(ok = warp_wait(&bar->sfull[s], i & 1, abort_flag, err))) break;
-      if (i > 0 && !(ok = warp_wait(&bar->adone[s], (i - 1) & 1, abort_flag, err))) break;  // P and dS are free again
+      if (KEYS) wait_warp(&bar->mfull[t % NS], (t / NS) & 1, abort_flag, err);
+      wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
+      if (i > 0) wait_warp(&bar->adone[s], (i - 1) & 1, abort_flag, err);  // P and dS are free again
       tc_fence_after();
       if (warp_on) {
-        const float2* st = reinterpret_cast<const float2*>(stats + (t % NS) * kStatBytes) + (KEYS ? (int)(stat_of(t) & 1) : 0);
+        const float* st = reinterpret_cast<const float*>(stats + (t % NS) * kStatBytes);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t a[32], b[32];
+          uint32_t a[32], b[32], u[16];
           tmem_ld_32x32b_x32(tmem + lanes + Tm::S(s) + h * 32, a);
           tmem_ld_32x32b_x32(tmem + lanes + Tm::dP(s) + h * 32, b);
           tmem_ld_wait();
-          if (some) {
-            // columns that take no part: weight 0 whatever the products left there
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 q = KEYS ? st[h * 32 + k] : make_float2(row_lse, row_d);
-              const bool on = w[h] >> k & 1u;
-              const float x = on ? ex2(fmaf(__uint_as_float(a[k]), p.c, -q.x)) : 0.f;
-              b[k] = on ? __float_as_uint(x * (__uint_as_float(b[k]) - q.y)) : 0u;
-              a[k] = __float_as_uint(x);
+          for (int k = 0; k < 32; k += 4) {
+            ulonglong2 nl = make_ulonglong2(row_lse, row_lse), nd = make_ulonglong2(row_d, row_d);
+            if constexpr (KEYS) {  // a row that takes no part has -lse = -inf there: weight 0
+              nl = *reinterpret_cast<const ulonglong2*>(st + h * 32 + k);
+              nd = *reinterpret_cast<const ulonglong2*>(st + kMove + h * 32 + k);
             }
-          } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 q = KEYS ? st[h * 32 + k] : make_float2(row_lse, row_d);
-              const float x = ex2(fmaf(__uint_as_float(a[k]), p.c, -q.x));
-              b[k] = __float_as_uint(x * (__uint_as_float(b[k]) - q.y));
-              a[k] = __float_as_uint(x);
+            for (int j = 0; j < 4; j += 2) {
+              float x, y;
+              unpack2(fma2(pack2(a[k + j], a[k + j + 1]), c2, j ? nl.y : nl.x), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              const f2 w = pack2(x, y);
+              const f2 z = mul2(w, add2(pack2(b[k + j], b[k + j + 1]), j ? nd.y : nd.x));
+              if constexpr (KEYS) a[(k + j) / 2] = pack_bf16(x, y);
+              unpack2(z, x, y);
+              u[(k + j) / 2] = pack_bf16(x, y);
             }
           }
-          uint32_t u[16];
           if constexpr (KEYS) {
+            uint32_t v[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = pack_bf16(__uint_as_float(a[2 * k]), __uint_as_float(a[2 * k + 1]));
-            tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, u);
+            for (int k = 0; k < 16; ++k) v[k] = a[k];
+            tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, v);
+          } else if (partial(t)) {
+            // keys that take no part: weight 0 whatever the products left there
+            if (h == 0) wait_warp(&bar->mready[t % NS], (t / NS) & 1, abort_flag, err);
+            const uint32_t w = bar->kept[t % NS][h];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] &= (w >> (2 * k) & 1u ? 0xffffu : 0u) | (w >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
           }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) u[k] = pack_bf16(__uint_as_float(b[2 * k]), __uint_as_float(b[2 * k + 1]));
           tmem_st_x16(tmem + lanes + Tm::dS(s) + h * 16, u);
         }
         tmem_st_wait();
@@ -823,10 +909,10 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       tc_fence_before();
       warp_arrive(&bar->pfull[s]);
     }
-    if (ok && nt > 0) ok = warp_wait(&bar->fin, 0, abort_flag, err);  // both streams' products are complete
+    if (nt > 0) wait_warp(&bar->fin, 0, abort_flag, err);  // both streams' products are complete
     tc_fence_after();
     // key pass: warpgroup 0 writes dV and 1 dK; query pass: each half of dQ's channels
-    if (ok && warp_on) {
+    if (warp_on) {
       const int64_t rows = KEYS ? (int64_t)p.nkv * p.Hkv : (int64_t)p.nq * p.Hq;
       const int64_t at = KEYS ? (int64_t)(f0 + row) * p.Hkv + hk : (int64_t)(f0 + row / p.r) * p.Hq + hk * p.r + row % p.r;
       const bool live = nt > 0 && !(KEYS && p.keep && row_on && p.keep[f0 + row] == 0);
@@ -874,7 +960,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
 }
 
 template <int DB>
-__global__ void __launch_bounds__(kFwdThreads, 1) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
   using Sh = BwdShape<DB>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -884,7 +970,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_bwd_kernel(const __grid_c
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bar->ffull, 1);
-    for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1);
+    for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1), mbar_init(&bar->mready[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4);
       mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
@@ -908,32 +994,42 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_bwd_kernel(const __grid_c
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// lse in base 2 and D = dO . O of every (query token, head), in the order of the packed rows of a key
-// head; 2^k lanes a row, 8 channels a lane.
+// -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
+// key pass reads them: group g's tiles start at tile q_off[g] / tokens + g, which leaves room for each
+// group's last, partly filled one.  Rows that do not exist, and rows without any key, get -inf and 0, so
+// that their weights vanish.  CTA (x, g): a tile and key head of group g; 2^k lanes a row, 8 channels a lane.
 __global__ void __launch_bounds__(256) attn_stat_kernel(const __nv_bfloat16* __restrict__ dO, const __nv_bfloat16* __restrict__ O,
-                                                        const float* __restrict__ lse, int nq, int Hq, int r, int d, int lanes,
-                                                        float2* __restrict__ stat) {
+                                                        const float* __restrict__ lse, const int32_t* __restrict__ q_off, int nq,
+                                                        int max_q, int Hq, int Hkv, int d, int lanes, int tiles,
+                                                        float* __restrict__ stat) {
   pdl_wait();
   pdl_trigger();
-  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / lanes;
+  const int g = blockIdx.y, hk = blockIdx.x % Hkv, t = blockIdx.x / Hkv, r = Hq / Hkv, tokens = kMove / r;
+  int q0, q1;
+  if (group_range(q_off, g, nq, max_q, q0, q1) & SVCONV_STATUS_BAD_OFFSETS) return;
+  if (t * tokens >= q1 - q0) return;
+  float* out = stat + ((int64_t)hk * tiles + q0 / tokens + g + t) * kStat;
   const int sub = threadIdx.x & (lanes - 1);
-  const bool on = row < (int64_t)nq * Hq;
-  float v = 0.f;
-  if (on && sub * 8 < d) {
-    const uint4 a = *reinterpret_cast<const uint4*>(dO + row * d + sub * 8), b = *reinterpret_cast<const uint4*>(O + row * d + sub * 8);
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  for (int row = threadIdx.x / lanes; row < kMove; row += 256 / lanes) {
+    const int token = q0 + t * tokens + row / r;
+    const bool on = row < tokens * r && token < q1;
+    const int64_t at = (int64_t)token * Hq + hk * r + row % r;
+    float v = 0.f;
+    if (on && sub * 8 < d) {
+      const uint4 a = *reinterpret_cast<const uint4*>(dO + at * d + sub * 8), b = *reinterpret_cast<const uint4*>(O + at * d + sub * 8);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), v);
-      v = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), v);
+      for (int i = 0; i < 4; ++i) {
+        v = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), v);
+        v = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), v);
+      }
     }
-  }
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (on && sub == 0) {
-    const int64_t token = row / Hq;
-    const int h = (int)(row - token * Hq);
-    const float l = lse[row];
-    stat[(int64_t)(h / r) * nq * r + token * r + h % r] = make_float2(l == -INFINITY ? INFINITY : l * kLog2e, v);
+    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (sub == 0) {
+      const float l = on ? lse[at] : -INFINITY;
+      out[row] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+      out[kMove + row] = on ? -v : 0.f;
+    }
   }
 }
 
@@ -1052,6 +1148,7 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
 // The same for the two passes of the backward call.
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits;
+  int tiles;            // of statistics, for each key head
   size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
   size_t floats() const { return stat + pq + 2 * pk; }
 };
@@ -1069,7 +1166,8 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
   b.qsplits = b.qblocks ? bwd_splits(heads * b.qblocks, cdiv(c.max_kv, kMove)) : 1;
   b.ksplits = b.kblocks ? bwd_splits(heads * b.kblocks, cdiv(c.max_q, kMove / r)) : 1;
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
-  b.stat = ((nq + 2 + kMove) * 2 + 3) / 4 * 4;  // a tile's copy may run past the last row
+  b.tiles = c.nq / (kMove / r) + c.G + 1;
+  b.stat = (size_t)b.tiles * c.Hkv * kStat;
   b.pq = b.qsplits > 1 ? b.qsplits * nq * c.d : 0;
   b.pk = b.ksplits > 1 ? b.ksplits * nk * c.d : 0;
   return b;
@@ -1079,14 +1177,14 @@ template <int DB>
 cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t s) {
   static int done[64];
   cudaError_t e = ensure_smem_attr(attn_bwd_kernel<DB>, BwdShape<DB>::kSmem, done);
-  return e == cudaSuccess ? launch_pdl(attn_bwd_kernel<DB>, dim3(grid), dim3(kFwdThreads), BwdShape<DB>::kSmem, s, p) : e;
+  return e == cudaSuccess ? launch_pdl(attn_bwd_kernel<DB>, dim3(grid), dim3(kThreads), BwdShape<DB>::kSmem, s, p) : e;
 }
 
 template <int DB>
 cudaError_t launch_fwd(const FwdParams& p, int grid, cudaStream_t s) {
   static int done[64];
   cudaError_t e = ensure_smem_attr(attn_fwd_kernel<DB>, FwdShape<DB>::kSmem, done);
-  return e == cudaSuccess ? launch_pdl(attn_fwd_kernel<DB>, dim3(grid), dim3(kFwdThreads), FwdShape<DB>::kSmem, s, p) : e;
+  return e == cudaSuccess ? launch_pdl(attn_fwd_kernel<DB>, dim3(grid), dim3(kThreads), FwdShape<DB>::kSmem, s, p) : e;
 }
 
 }  // namespace
@@ -1167,7 +1265,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   const int r = c.Hq / c.Hkv;
   int lanes = 1;
   while (lanes < c.d / 8) lanes *= 2;
-  const long long stat_grid = ((long long)c.nq * c.Hq * lanes + 255) / 256;
+  const long long stat_grid = (long long)cdiv(c.max_q, kMove / r) * c.Hkv;
   if (q_items + k_items > 0x7fffffffLL || stat_grid > 0x7fffffffLL) return SVCONV_ERR_SIZE;
   float* ws = static_cast<float*>(workspace);
   BwdParams p{};
@@ -1177,8 +1275,8 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   p.q_items = (int)q_items;
   p.c = c.scale * kLog2e;
   p.scale = c.scale;
-  float2* stat = reinterpret_cast<float2*>(ws);
-  p.stat = stat;
+  p.stat = ws;
+  p.stat_tiles = b.tiles;
   p.part_q = ws + b.stat;
   p.part_k = p.part_q + b.pq;
   p.part_v = p.part_k + b.pk;
@@ -1200,9 +1298,9 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (c.nq > 0)
-    e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
-                   static_cast<const __nv_bfloat16*>(O), lse, c.nq, c.Hq, r, c.d, lanes, stat);
+  if (c.max_q > 0)
+    e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid, c.G), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
+                   static_cast<const __nv_bfloat16*>(O), lse, c.q_off, c.nq, c.max_q, c.Hq, c.Hkv, c.d, lanes, b.tiles, ws);
   if (e == cudaSuccess)
     e = c.d <= 64 ? launch_bwd<1>(p, (int)(q_items + k_items), s) : launch_bwd<2>(p, (int)(q_items + k_items), s);
   auto add = [&](const float* part, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound, int H,
