@@ -127,6 +127,39 @@ __device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, volati
   wait_for(bar, parity, abort_flag, err);
   __syncwarp();
 }
+// A value that is the same in every lane, told to the compiler as such: what depends on it stays in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Products and commits issued by the one lane with e != 0 of a converged warp.  Predicated instead of branched
+// around, so that descriptors and addresses are warp-uniform and sit in uniform registers when the instruction
+// wants them there (in a branch of one lane each operand was moved over first: ~100 cycles a product).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t e) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t e) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint32_t e) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(e)
+      : "memory");
+}
+
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -231,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   const uint32_t sq = base, skv = base + 2 * Sh::kTileBytes;
   FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(aligned + (2 + NS) * (size_t)Sh::kTileBytes);
   volatile int* abort_flag = &bar->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   // work item: query block fastest, so CTAs that run together share keys in L2
   int item = blockIdx.x;
@@ -297,74 +330,69 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     }
   } else if (warp == kMmaWarp) {
     if (nt > 0) {
+      const uint32_t e = lane == 0;
       const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
       const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, 0, 0), idesc_o = idesc_bf16_f32(kTile, dn, 0, 1);
+      const uint32_t tm = uniform(tmem);
+      const int steps0 = uniform(steps_of(0)), steps1 = uniform(steps_of(1));
+      const bool pair = p.pair, lone = steps1 == 0;
+      const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(skv, 16, 1024),
+                     dv = smem_desc_sw128(skv, kBlockBytes, 1024);
       int k_seen = -1, v_seen = -1;  // newest K / V tile known to have landed
-      auto seen = [&](int& newest, int tile, int which) {
-        if (tile <= newest) return;
-        newest = tile;
-        const int n = 2 * tile + which;
-        // rows of V behind the group's end or dropped by the mask must be zero: their weights are
-        wait_warp(which && masked(tile) ? &bar->vready[n % NS] : &bar->kvfull[n % NS], (n / NS) & 1, abort_flag, err);
-      };
       auto issue_s = [&](int s, int i) {
-        const int tile = tile_of(s, i);
-        seen(k_seen, tile, 0);
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t a0 = smem_desc_sw128(sq + (p.pair ? s : 0) * Sh::kTileBytes, 16, 1024);
-          const uint64_t b0 = smem_desc_sw128(skv + (2 * tile % NS) * Sh::kTileBytes, 16, 1024);
-          for (int k = 0; k < ks; ++k) {
-            const uint64_t at = (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
-            tc_mma_bf16(tmem + Sh::kS(s), a0 + at, b0 + at, idesc_s, k ? 1u : 0u);
-          }
-          tc_commit(&bar->sfull[s]);
-          // the tile's last reader frees it (pair form: the second stream, where it has rows)
-          if (!p.pair || s == 1 || steps_of(1) == 0) tc_commit(&bar->kvempty[2 * tile % NS]);
+        const int tile = pair ? i : 2 * i + s, n = 2 * tile, slot = n % NS;
+        if (tile > k_seen) {
+          k_seen = tile;
+          wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
         }
-        __syncwarp();
+        tc_fence_after();
+        const uint64_t a0 = dq + (uint64_t)(pair && s ? Sh::kTileBytes >> 4 : 0), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < 4 * DB; ++k) {
+          const uint64_t at = (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
+          if (k < ks) mma_ss(tm + Sh::kS(0) + s * (Sh::kS(1) - Sh::kS(0)), a0 + at, b0 + at, idesc_s, k ? 1u : 0u, e);
+        }
+        commit_to(&bar->sfull[s], e);
+        // the tile's last reader frees it (pair form: the second stream, where it has rows)
+        commit_to(&bar->kvempty[slot], e && (!pair || s == 1 || lone));
       };
       auto issue_o = [&](int s, int i) {
-        const int tile = tile_of(s, i);
-        seen(v_seen, tile, 1);
-        if (lane == 0) {
-          tc_fence_after();
-          const int slot = (2 * tile + 1) % NS;
-          const uint64_t b0 = smem_desc_sw128(skv + slot * Sh::kTileBytes, kBlockBytes, 1024);
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_bf16_ts(tmem + Sh::kO(s), tmem + Sh::kP(s) + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_o, (i | k) ? 1u : 0u);
-          tc_commit(&bar->odone[s]);
-          if (!p.pair || s == 1 || steps_of(1) == 0) tc_commit(&bar->kvempty[slot]);
+        const int tile = pair ? i : 2 * i + s, n = 2 * tile + 1, slot = n % NS;
+        if (tile > v_seen) {
+          v_seen = tile;
+          // rows of V behind the group's end or dropped by the mask must be zero: their weights are
+          wait_warp(masked(tile) ? &bar->vready[slot] : &bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
         }
-        __syncwarp();
+        tc_fence_after();
+        const uint64_t b0 = dv + (uint64_t)(slot * (Sh::kTileBytes >> 4));
+        const uint32_t o = tm + Sh::kO(0) + s * (Sh::kO(1) - Sh::kO(0)), pr = tm + Sh::kP(0) + s * (Sh::kP(1) - Sh::kP(0));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) mma_ts(o, pr + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_o, (i | k) ? 1u : 0u, e);
+        commit_to(&bar->odone[s], e);
+        commit_to(&bar->kvempty[slot], e && (!pair || s == 1 || lone));
       };
       wait_warp(&bar->qfull, 0, abort_flag, err);
-      for (int s = 0; s < 2; ++s)
-        if (steps_of(s) > 0) issue_s(s, 0);
-      const int steps = steps_of(0);
-      for (int i = 0; i < steps; ++i)
+      issue_s(0, 0);
+      if (steps1 > 0) issue_s(1, 0);
+      for (int i = 0; i < steps0; ++i)
+#pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (i >= steps_of(s)) continue;
+          const int steps = s ? steps1 : steps0;
+          if (i >= steps) continue;
           wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
-          const bool more = i + 1 < steps_of(s);
           if constexpr (DB == 1) {
-            if (more) issue_s(s, i + 1);
+            if (i + 1 < steps) issue_s(s, i + 1);
             issue_o(s, i);
           } else {
             issue_o(s, i);
-            if (more) {
+            if (i + 1 < steps) {
               wait_warp(&bar->odone[s], i & 1, abort_flag, err);  // P shares S's columns
               issue_s(s, i + 1);
             }
           }
         }
-      if (lane == 0) {  // every issued product is complete before tensor memory is released
-        tc_commit(&bar->fin);
-        volatile int never = 0;
-        mbar_wait(&bar->fin, 0, &never, err, kDefaultTimeoutNs);
-      }
-      __syncwarp();
+      commit_to(&bar->fin, e);
+      wait_warp(&bar->fin, 0, abort_flag, err);  // every issued product is complete before tensor memory is released
     }
   } else if (warp == kCheckWarp) {
     for (int tile = 0; tile < nt; ++tile) {
@@ -678,7 +706,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
   using Sh = BwdShape<DB>;
   using Tm = BwdTmem<DB, KEYS>;
   constexpr int NS = Sh::kStages;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bar->abort_flag;
   int* err = p.status;
   const uint32_t sf = base, sm = base + 2 * Sh::kFixedBytes;
@@ -755,79 +783,77 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
     }
   } else if (warp == kMmaWarp) {
     if (nt > 0) {
+      const uint32_t e = lane == 0;
       const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
       const uint32_t idesc_s = idesc_bf16_f32(kTile, kMove, 0, 0), idesc_a = idesc_bf16_f32(kTile, dn, 0, 1);
-      wait_warp(&bar->ffull, 0, abort_flag, err);
-      // operand o of the scores of tile t into column col
-      auto scores = [&](int o, int t, int col) {
-        const uint64_t a0 = smem_desc_sw128(sf + o * Sh::kFixedBytes, 16, 1024);
-        const uint64_t b0 = smem_desc_sw128(sm + (t % NS) * Sh::kStageBytes + o * Sh::kMoveBytes, 16, 1024);
-        for (int k = 0; k < ks; ++k)
-          tc_mma_bf16(tmem + col, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2),
-                      b0 + (uint64_t)((k >> 2) * (kMoveBlock >> 4) + (k & 3) * 2), idesc_s, k ? 1u : 0u);
-      };
-      // acc += A (tensor memory) x operand o of tile t
-      auto sums = [&](int o, int t, int a_col, int acc) {
-        const uint64_t b0 = smem_desc_sw128(sm + (t % NS) * Sh::kStageBytes + o * Sh::kMoveBytes, kMoveBlock, 1024);
+      const uint32_t tm = uniform(tmem);
+      const int n = uniform(nt);
+      const uint64_t df = smem_desc_sw128(sf, 16, 1024), dm = smem_desc_sw128(sm, 16, 1024), dt = smem_desc_sw128(sm, kMoveBlock, 1024);
+      // scores of operand o (0: F1 M1, 1: F2 M2) of the tile in this slot
+      auto scores = [&](int o, int slot, uint32_t d) {
+        const uint64_t a0 = df + (uint64_t)(o * (Sh::kFixedBytes >> 4)), b0 = dm + (uint64_t)(slot * (Sh::kStageBytes >> 4) + o * (Sh::kMoveBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < kMove / 16; ++k)
-          tc_mma_bf16_ts(tmem + acc, tmem + a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_a, (t | k) ? 1u : 0u);
+        for (int k = 0; k < 4 * DB; ++k)
+          if (k < ks)
+            mma_ss(d, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), b0 + (uint64_t)((k >> 2) * (kMoveBlock >> 4) + (k & 3) * 2),
+                   idesc_s, k ? 1u : 0u, e);
+      };
+      // acc += A (tensor memory) x operand o of the tile in this slot
+      auto sums = [&](int o, int slot, uint32_t a_col, uint32_t acc, bool more) {
+        const uint64_t b0 = dt + (uint64_t)(slot * (Sh::kStageBytes >> 4) + o * (Sh::kMoveBytes >> 4));
+#pragma unroll
+        for (int k = 0; k < kMove / 16; ++k) mma_ts(acc, a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_a, more || k ? 1u : 0u, e);
       };
       auto landed = [&](int t) {  // rows that take no part are zero by then: they meet zero weights
         wait_warp(partial(t) ? &bar->mready[t % NS] : &bar->mfull[t % NS], (t / NS) & 1, abort_flag, err);
         tc_fence_after();
       };
+      wait_warp(&bar->ffull, 0, abort_flag, err);
+#pragma unroll
       for (int s = 0; s < 2; ++s)
-        if (steps_of(s) > 0) {
+        if (s < n) {
           landed(s);
-          if (lane == 0) {
-            scores(0, s, Tm::S(s));
-            scores(1, s, Tm::dP(s));
-            tc_commit(&bar->sfull[s]);
-          }
-          __syncwarp();
+          scores(0, s, tm + Tm::S(s));
+          scores(1, s, tm + Tm::dP(s));
+          commit_to(&bar->sfull[s], e);
         }
-      for (int t = 0; t < nt; ++t) {
-        const int s = t & 1, ph = (t >> 1) & 1, next = t + 2;
-        wait_warp(&bar->pfull[s], ph, abort_flag, err);
-        if (next < nt) landed(next);
-        if (lane == 0) {
+      for (int t0 = 0; t0 < n; t0 += 2)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int t = t0 + s, ph = (t0 >> 1) & 1, next = t + 2, slot = t % NS, nslot = next % NS;
+          if (t >= n) continue;
+          wait_warp(&bar->pfull[s], ph, abort_flag, err);
+          if (next < n) landed(next);
           tc_fence_after();
           if constexpr (Tm::kShared) {
             // P and dS lie in the columns of the next scores: each product is waited for before its
             // columns are written, the other product keeping the pipe busy meanwhile
-            sums(1, t, Tm::P(s), Tm::kAcc1);
-            tc_commit(&bar->pdone[s]);
-            sums(0, t, Tm::dS(s), Tm::kAcc2);
-            tc_commit(&bar->adone[s]);
-            tc_commit(&bar->mempty[t % NS]);
-            if (next < nt) {
-              wait_for(&bar->pdone[s], ph, abort_flag, err);
-              scores(0, next, Tm::S(s));
-              wait_for(&bar->adone[s], ph, abort_flag, err);
-              scores(1, next, Tm::dP(s));
-              tc_commit(&bar->sfull[s]);
+            sums(1, slot, tm + Tm::P(s), tm + Tm::kAcc1, t > 0);
+            commit_to(&bar->pdone[s], e);
+            sums(0, slot, tm + Tm::dS(s), tm + Tm::kAcc2, t > 0);
+            commit_to(&bar->adone[s], e);
+            commit_to(&bar->mempty[slot], e);
+            if (next < n) {
+              wait_warp(&bar->pdone[s], ph, abort_flag, err);
+              scores(0, nslot, tm + Tm::S(s));
+              wait_warp(&bar->adone[s], ph, abort_flag, err);
+              scores(1, nslot, tm + Tm::dP(s));
+              commit_to(&bar->sfull[s], e);
             }
           } else {
-            if (next < nt) {
-              scores(0, next, Tm::S(s));
-              scores(1, next, Tm::dP(s));
-              tc_commit(&bar->sfull[s]);
+            if (next < n) {
+              scores(0, nslot, tm + Tm::S(s));
+              scores(1, nslot, tm + Tm::dP(s));
+              commit_to(&bar->sfull[s], e);
             }
-            if constexpr (KEYS) sums(1, t, Tm::P(s), Tm::kAcc1);
-            sums(0, t, Tm::dS(s), Tm::kAcc2);
-            tc_commit(&bar->adone[s]);
-            tc_commit(&bar->mempty[t % NS]);
+            if constexpr (KEYS) sums(1, slot, tm + Tm::P(s), tm + Tm::kAcc1, t > 0);
+            sums(0, slot, tm + Tm::dS(s), tm + Tm::kAcc2, t > 0);
+            commit_to(&bar->adone[s], e);
+            commit_to(&bar->mempty[slot], e);
           }
         }
-        __syncwarp();
-      }
-      if (lane == 0) {  // every issued product is complete before tensor memory is released
-        tc_commit(&bar->fin);
-        volatile int never = 0;
-        mbar_wait(&bar->fin, 0, &never, err, kDefaultTimeoutNs);
-      }
-      __syncwarp();
+      commit_to(&bar->fin, e);
+      wait_warp(&bar->fin, 0, abort_flag, err);  // every issued product is complete before tensor memory is released
     }
   } else if (warp == kCheckWarp) {
     for (int t = 0; t < nt; ++t) {
