@@ -36,9 +36,12 @@ __device__ __forceinline__ int group_range(const int32_t* off, int g, int n, int
 constexpr int kTile = 128;             // query rows (query tokens x their r heads) and keys of a tile
 constexpr int kBlockBytes = kTile * 128;  // 128 rows of 64 bf16 channels, 128-byte swizzled
 constexpr int kSoftWarps = 8;          // two softmax warpgroups, one per stream
-constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kCheckWarp = kSoftWarps + 2;  // zeroes rows that take no part, ahead of the products
-constexpr int kThreads = (kSoftWarps + 3) * 32;
+constexpr int kLoadWarp = kSoftWarps;
+constexpr int kCheckWarp = kSoftWarps + 1;  // zeroes rows that take no part, ahead of the products
+// Two warps issue products, one the scores and one the sums (P V; dS K and the like): a warp's first shared-memory
+// access after a batch of products waits ~200 cycles for them, which then overlaps the other warp's.
+constexpr int kScoreWarp = kSoftWarps + 2, kSumWarp = kSoftWarps + 3;
+constexpr int kThreads = (kSoftWarps + 4) * 32;
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
   asm volatile(
@@ -237,7 +240,7 @@ struct FwdParams {
 };
 
 struct FwdBarriers {
-  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], pfull[2], odone[2], fin;
+  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], pfull[2], odone[2], fin[2];
   uint32_t kept[10][4];  // keys that take part, of the tile whose V lies in this slot
   uint32_t tmem;
   int abort_flag;
@@ -278,12 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     mbar_init(&bar->qfull, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4), mbar_init(&bar->odone[s], 1);
-    mbar_init(&bar->fin, 1);
+    mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
     bar->abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&p.tq), prefetch_tmap(&p.tk), prefetch_tmap(&p.tv);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kSumWarp) {
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
@@ -328,71 +331,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                       k0 + (t_lo + loaded / 2) * kTile);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kScoreWarp) {
     if (nt > 0) {
       const uint32_t e = lane == 0;
-      const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, 0, 0), idesc_o = idesc_bf16_f32(kTile, dn, 0, 1);
-      const uint32_t tm = uniform(tmem);
+      const int ks = (p.d + 15) / 16;
+      const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 0, 0), tm = uniform(tmem);
       const int steps0 = uniform(steps_of(0)), steps1 = uniform(steps_of(1));
       const bool pair = p.pair, lone = steps1 == 0;
-      const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(skv, 16, 1024),
-                     dv = smem_desc_sw128(skv, kBlockBytes, 1024);
-      int k_seen = -1, v_seen = -1;  // newest K / V tile known to have landed
-      auto issue_s = [&](int s, int i) {
-        const int tile = pair ? i : 2 * i + s, n = 2 * tile, slot = n % NS;
-        if (tile > k_seen) {
-          k_seen = tile;
-          wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
-        }
-        tc_fence_after();
-        const uint64_t a0 = dq + (uint64_t)(pair && s ? Sh::kTileBytes >> 4 : 0), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
-#pragma unroll
-        for (int k = 0; k < 4 * DB; ++k) {
-          const uint64_t at = (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
-          if (k < ks) mma_ss(tm + Sh::kS(0) + s * (Sh::kS(1) - Sh::kS(0)), a0 + at, b0 + at, idesc_s, k ? 1u : 0u, e);
-        }
-        commit_to(&bar->sfull[s], e);
-        // the tile's last reader frees it (pair form: the second stream, where it has rows)
-        commit_to(&bar->kvempty[slot], e && (!pair || s == 1 || lone));
-      };
-      auto issue_o = [&](int s, int i) {
-        const int tile = pair ? i : 2 * i + s, n = 2 * tile + 1, slot = n % NS;
-        if (tile > v_seen) {
-          v_seen = tile;
-          // rows of V behind the group's end or dropped by the mask must be zero: their weights are
-          wait_warp(masked(tile) ? &bar->vready[slot] : &bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
-        }
-        tc_fence_after();
-        const uint64_t b0 = dv + (uint64_t)(slot * (Sh::kTileBytes >> 4));
-        const uint32_t o = tm + Sh::kO(0) + s * (Sh::kO(1) - Sh::kO(0)), pr = tm + Sh::kP(0) + s * (Sh::kP(1) - Sh::kP(0));
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) mma_ts(o, pr + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_o, (i | k) ? 1u : 0u, e);
-        commit_to(&bar->odone[s], e);
-        commit_to(&bar->kvempty[slot], e && (!pair || s == 1 || lone));
-      };
+      const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(skv, 16, 1024);
       wait_warp(&bar->qfull, 0, abort_flag, err);
-      issue_s(0, 0);
-      if (steps1 > 0) issue_s(1, 0);
       for (int i = 0; i < steps0; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int steps = s ? steps1 : steps0;
-          if (i >= steps) continue;
-          wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
-          if constexpr (DB == 1) {
-            if (i + 1 < steps) issue_s(s, i + 1);
-            issue_o(s, i);
-          } else {
-            issue_o(s, i);
-            if (i + 1 < steps) {
-              wait_warp(&bar->odone[s], i & 1, abort_flag, err);  // P shares S's columns
-              issue_s(s, i + 1);
-            }
+          if (i >= (s ? steps1 : steps0)) continue;
+          const int tile = pair ? i : 2 * i + s, n = 2 * tile, slot = n % NS;
+          // S is free once its scores have been read; where P lies in its columns, once P V is done too
+          if (i > 0) wait_warp(DB == 1 ? &bar->pfull[s] : &bar->odone[s], (i - 1) & 1, abort_flag, err);
+          if (!pair || s == 0) wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
+          tc_fence_after();
+          const uint64_t a0 = dq + (uint64_t)(pair && s ? Sh::kTileBytes >> 4 : 0), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < 4 * DB; ++k) {
+            const uint64_t at = (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
+            if (k < ks) mma_ss(tm + Sh::kS(s), a0 + at, b0 + at, idesc, k ? 1u : 0u, e);
           }
+          commit_to(&bar->sfull[s], e);
+          // the tile's last reader frees it (pair form: the second stream, where it has rows)
+          if (!pair || s == 1 || lone) commit_to(&bar->kvempty[slot], e);
         }
-      commit_to(&bar->fin, e);
-      wait_warp(&bar->fin, 0, abort_flag, err);  // every issued product is complete before tensor memory is released
+      commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
+      wait_warp(&bar->fin[0], 0, abort_flag, err);
+    }
+  } else if (warp == kSumWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const uint32_t idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), tm = uniform(tmem);
+      const int steps0 = uniform(steps_of(0)), steps1 = uniform(steps_of(1));
+      const bool pair = p.pair, lone = steps1 == 0;
+      const uint64_t dv = smem_desc_sw128(skv, kBlockBytes, 1024);
+      for (int i = 0; i < steps0; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (i >= (s ? steps1 : steps0)) continue;
+          const int tile = pair ? i : 2 * i + s, n = 2 * tile + 1, slot = n % NS;
+          // rows of V behind the group's end or dropped by the mask must be zero: their weights are
+          if (!pair || s == 0) wait_warp(masked(tile) ? &bar->vready[slot] : &bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
+          wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
+          tc_fence_after();
+          const uint64_t b0 = dv + (uint64_t)(slot * (Sh::kTileBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tm + Sh::kO(s), tm + Sh::kP(s) + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc, (i | k) ? 1u : 0u, e);
+          commit_to(&bar->odone[s], e);
+          if (!pair || s == 1 || lone) commit_to(&bar->kvempty[slot], e);
+        }
+      commit_to(&bar->fin[1], e);
+      wait_warp(&bar->fin[1], 0, abort_flag, err);
     }
   } else if (warp == kCheckWarp) {
     for (int tile = 0; tile < nt; ++tile) {
@@ -585,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     for (int i = loaded > NS ? loaded - NS : 0; i < loaded; ++i)
       mbar_wait(&bar->kvfull[i % NS], (i / NS) & 1, &never, err, kDefaultTimeoutNs);
   }
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
 // The splits of each (row, head) merged in a fixed order: a warp takes every 8th split, then the
@@ -673,7 +667,7 @@ struct BwdParams {
 };
 
 struct BwdBarriers {
-  uint64_t ffull, mfull[8], mempty[8], mready[8], sfull[2], pfull[2], pdone[2], adone[2], fin;
+  uint64_t ffull, mfull[8], mempty[8], mready[8], sfull[2], pfull[2], pdone[2], adone[2], fin[2];
   uint32_t kept[8][2];  // query pass: keys of the slot's tile that take part
   uint32_t tmem;
   int abort_flag;
@@ -781,79 +775,73 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
           bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kScoreWarp) {
     if (nt > 0) {
       const uint32_t e = lane == 0;
-      const int dn = (p.d + 15) / 16 * 16, ks = dn / 16;
-      const uint32_t idesc_s = idesc_bf16_f32(kTile, kMove, 0, 0), idesc_a = idesc_bf16_f32(kTile, dn, 0, 1);
-      const uint32_t tm = uniform(tmem);
-      const int n = uniform(nt);
-      const uint64_t df = smem_desc_sw128(sf, 16, 1024), dm = smem_desc_sw128(sm, 16, 1024), dt = smem_desc_sw128(sm, kMoveBlock, 1024);
-      // scores of operand o (0: F1 M1, 1: F2 M2) of the tile in this slot
+      const int ks = (p.d + 15) / 16, n = uniform(nt);
+      const uint32_t idesc = idesc_bf16_f32(kTile, kMove, 0, 0), tm = uniform(tmem);
+      const uint64_t df = smem_desc_sw128(sf, 16, 1024), dm = smem_desc_sw128(sm, 16, 1024);
+      // operand o (0: F1 M1, 1: F2 M2) of the tile in this slot
       auto scores = [&](int o, int slot, uint32_t d) {
         const uint64_t a0 = df + (uint64_t)(o * (Sh::kFixedBytes >> 4)), b0 = dm + (uint64_t)(slot * (Sh::kStageBytes >> 4) + o * (Sh::kMoveBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 4 * DB; ++k)
           if (k < ks)
             mma_ss(d, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), b0 + (uint64_t)((k >> 2) * (kMoveBlock >> 4) + (k & 3) * 2),
-                   idesc_s, k ? 1u : 0u, e);
+                   idesc, k ? 1u : 0u, e);
       };
+      wait_warp(&bar->ffull, 0, abort_flag, err);
+      for (int t0 = 0; t0 < n; t0 += 2)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int t = t0 + s, ph = ((t0 >> 1) - 1) & 1, slot = t % NS;
+          if (t >= n) continue;
+          // rows that take no part are zero by then: they meet zero weights
+          wait_warp(partial(t) ? &bar->mready[slot] : &bar->mfull[slot], (t / NS) & 1, abort_flag, err);
+          // the scores' columns are free once they have been read; where P and dS lie in them, once the sums
+          // that read those are done
+          if (t0 > 0) wait_warp(Tm::kShared ? &bar->pdone[s] : &bar->pfull[s], ph, abort_flag, err);
+          tc_fence_after();
+          scores(0, slot, tm + Tm::S(s));
+          if (Tm::kShared && t0 > 0) {
+            wait_warp(&bar->adone[s], ph, abort_flag, err);
+            tc_fence_after();
+          }
+          scores(1, slot, tm + Tm::dP(s));
+          commit_to(&bar->sfull[s], e);
+        }
+      commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
+      wait_warp(&bar->fin[0], 0, abort_flag, err);
+    }
+  } else if (warp == kSumWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const int n = uniform(nt);
+      const uint32_t idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), tm = uniform(tmem);
+      const uint64_t dt = smem_desc_sw128(sm, kMoveBlock, 1024);
       // acc += A (tensor memory) x operand o of the tile in this slot
       auto sums = [&](int o, int slot, uint32_t a_col, uint32_t acc, bool more) {
         const uint64_t b0 = dt + (uint64_t)(slot * (Sh::kStageBytes >> 4) + o * (Sh::kMoveBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < kMove / 16; ++k) mma_ts(acc, a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc_a, more || k ? 1u : 0u, e);
+        for (int k = 0; k < kMove / 16; ++k) mma_ts(acc, a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc, more || k ? 1u : 0u, e);
       };
-      auto landed = [&](int t) {  // rows that take no part are zero by then: they meet zero weights
-        wait_warp(partial(t) ? &bar->mready[t % NS] : &bar->mfull[t % NS], (t / NS) & 1, abort_flag, err);
-        tc_fence_after();
-      };
-      wait_warp(&bar->ffull, 0, abort_flag, err);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s < n) {
-          landed(s);
-          scores(0, s, tm + Tm::S(s));
-          scores(1, s, tm + Tm::dP(s));
-          commit_to(&bar->sfull[s], e);
-        }
       for (int t0 = 0; t0 < n; t0 += 2)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const int t = t0 + s, ph = (t0 >> 1) & 1, next = t + 2, slot = t % NS, nslot = next % NS;
+          const int t = t0 + s, slot = t % NS;
           if (t >= n) continue;
-          wait_warp(&bar->pfull[s], ph, abort_flag, err);
-          if (next < n) landed(next);
+          wait_warp(&bar->pfull[s], (t0 >> 1) & 1, abort_flag, err);  // the tile itself landed before its scores
           tc_fence_after();
-          if constexpr (Tm::kShared) {
-            // P and dS lie in the columns of the next scores: each product is waited for before its
-            // columns are written, the other product keeping the pipe busy meanwhile
+          if constexpr (KEYS) {
             sums(1, slot, tm + Tm::P(s), tm + Tm::kAcc1, t > 0);
-            commit_to(&bar->pdone[s], e);
-            sums(0, slot, tm + Tm::dS(s), tm + Tm::kAcc2, t > 0);
-            commit_to(&bar->adone[s], e);
-            commit_to(&bar->mempty[slot], e);
-            if (next < n) {
-              wait_warp(&bar->pdone[s], ph, abort_flag, err);
-              scores(0, nslot, tm + Tm::S(s));
-              wait_warp(&bar->adone[s], ph, abort_flag, err);
-              scores(1, nslot, tm + Tm::dP(s));
-              commit_to(&bar->sfull[s], e);
-            }
-          } else {
-            if (next < n) {
-              scores(0, nslot, tm + Tm::S(s));
-              scores(1, nslot, tm + Tm::dP(s));
-              commit_to(&bar->sfull[s], e);
-            }
-            if constexpr (KEYS) sums(1, slot, tm + Tm::P(s), tm + Tm::kAcc1, t > 0);
-            sums(0, slot, tm + Tm::dS(s), tm + Tm::kAcc2, t > 0);
-            commit_to(&bar->adone[s], e);
-            commit_to(&bar->mempty[slot], e);
+            if constexpr (Tm::kShared) commit_to(&bar->pdone[s], e);
           }
+          sums(0, slot, tm + Tm::dS(s), tm + Tm::kAcc2, t > 0);
+          commit_to(&bar->adone[s], e);
+          commit_to(&bar->mempty[slot], e);
         }
-      commit_to(&bar->fin, e);
-      wait_warp(&bar->fin, 0, abort_flag, err);  // every issued product is complete before tensor memory is released
+      commit_to(&bar->fin[1], e);
+      wait_warp(&bar->fin[1], 0, abort_flag, err);
     }
   } else if (warp == kCheckWarp) {
     for (int t = 0; t < nt; ++t) {
@@ -935,7 +923,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       tc_fence_before();
       warp_arrive(&bar->pfull[s]);
     }
-    if (nt > 0) wait_warp(&bar->fin, 0, abort_flag, err);  // both streams' products are complete
+    if (nt > 0) wait_warp(&bar->fin[1], 0, abort_flag, err);  // both streams' sums are complete
     tc_fence_after();
     // key pass: warpgroup 0 writes dV and 1 dK; query pass: each half of dQ's channels
     if (warp_on) {
@@ -1001,11 +989,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
       mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4);
       mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
     }
-    mbar_init(&bar->fin, 1);
+    mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
     bar->abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kSumWarp) {
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
@@ -1017,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
   pdl_trigger();
   if ((int)blockIdx.x < p.q_items) bwd_pass<DB, false>(p, blockIdx.x, base, bar, stats);
   else bwd_pass<DB, true>(p, blockIdx.x - p.q_items, base, bar, stats);
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
 // -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
