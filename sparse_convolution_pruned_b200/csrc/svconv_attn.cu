@@ -240,7 +240,7 @@ struct FwdParams {
 };
 
 struct FwdBarriers {
-  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], pfull[2], odone[2], fin[2];
+  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], sread[2], pfull[2], odone[2], fin[2];
   uint32_t kept[10][4];  // keys that take part, of the tile whose V lies in this slot
   uint32_t tmem;
   int abort_flag;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     mbar_init(&bar->qfull, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4), mbar_init(&bar->odone[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 4), mbar_init(&bar->pfull[s], 4), mbar_init(&bar->odone[s], 1);
     mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
     bar->abort_flag = 0;
     fence_barrier_init();
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           if (i >= (s ? steps1 : steps0)) continue;
           const int tile = pair ? i : 2 * i + s, n = 2 * tile, slot = n % NS;
           // S is free once its scores have been read; where P lies in its columns, once P V is done too
-          if (i > 0) wait_warp(DB == 1 ? &bar->pfull[s] : &bar->odone[s], (i - 1) & 1, abort_flag, err);
+          if (i > 0) wait_warp(DB == 1 ? &bar->sread[s] : &bar->odone[s], (i - 1) & 1, abort_flag, err);
           if (!pair || s == 0) wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
           tc_fence_after();
           const uint64_t a0 = dq + (uint64_t)(pair && s ? Sh::kTileBytes >> 4 : 0), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
@@ -417,11 +417,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       const bool some = masked(tile);
       wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
       tc_fence_after();
+      uint32_t v[4][32];
       if (warp_on) {
-        uint32_t v[4][32];
 #pragma unroll
         for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(tmem + lanes + Sh::kS(s) + b * 32, v[b]);
-        tmem_ld_wait();
+      }
+      if constexpr (DB == 1) {
+        // P's columns and O are free again; at 128 channels these scores already waited for that
+        if (i > 0) wait_warp(&bar->odone[s], (i - 1) & 1, abort_flag, err);
+      }
+      tmem_ld_wait();
+      if constexpr (DB == 1) {
+        // the scores are in registers: the next ones may be computed over them
+        tc_fence_before();
+        warp_arrive(&bar->sread[s]);
+      }
+      if (warp_on) {
         if (p.c < 0.f) {
 #pragma unroll
           for (int b = 0; b < 4; ++b)
@@ -452,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         if (m == -INFINITY || (tile_max - m) * ca > kRescaleLog2) m = fmaxf(m, tile_max);
         const float mm = m == -INFINITY ? 0.f : m * ca;
         if (i > 0) {
-          wait_warp(&bar->odone[s], (i - 1) & 1, abort_flag, err);
           tc_fence_after();
           if (__any_sync(0xffffffffu, m != m_old)) {
             const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
