@@ -35,7 +35,7 @@ __device__ __forceinline__ int group_range(const int32_t* off, int g, int n, int
 // ============================================================================ tensor-core building blocks
 constexpr int kTile = 128;             // query rows (query tokens x their r heads) and keys of a tile
 constexpr int kBlockBytes = kTile * 128;  // 128 rows of 64 bf16 channels, 128-byte swizzled
-constexpr int kSoftWarps = 8;          // two softmax warpgroups, one per stream
+constexpr int kSoftWarps = 16;         // four softmax warpgroups: two per stream, half of a tile's columns each
 constexpr int kLoadWarp = kSoftWarps;
 constexpr int kCheckWarp = kSoftWarps + 1;  // zeroes rows that take no part, ahead of the products
 // Two warps issue products, one the scores and one the sums (P V; dS K and the like): a warp's first shared-memory
@@ -125,8 +125,9 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
     }
   }
 }
-// The whole warp waits, and is converged afterwards.
+// The whole warp waits, and is converged afterwards; mostly the first try succeeds, and a vote is all it takes.
 __device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
   wait_for(bar, parity, abort_flag, err);
   __syncwarp();
 }
@@ -242,6 +243,7 @@ struct FwdParams {
 struct FwdBarriers {
   uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], sread[2], pfull[2], odone[2], fin[2];
   uint32_t kept[10][4];  // keys that take part, of the tile whose V lies in this slot
+  float rowmax[2][2][2][kTile];  // [step parity][stream][half of the columns][row], exchanged between the halves
   uint32_t tmem;
   int abort_flag;
 };
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     mbar_init(&bar->qfull, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 4), mbar_init(&bar->pfull[s], 4), mbar_init(&bar->odone[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8), mbar_init(&bar->odone[s], 1);
     mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
     bar->abort_flag = 0;
     fence_barrier_init();
@@ -403,24 +405,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       warp_arrive(&bar->vready[slot]);
     }
   } else {
-    // ------------------------------------------------------------ softmax: one thread per row
-    const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+    // ------------------------------------------------------------ softmax: two threads per row, 64 scores each
+    const int s = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int pair_bar = 1 + s * 4 + (warp & 3);  // named barrier of the two warps that hold the same rows
     const int stok0 = tok0 + (p.pair ? s * p.tokens : 0);
     const int left = work ? min(p.tokens, q1 - stok0) * p.r : 0;
     const bool warp_on = (warp & 3) * 32 < left, row_on = row < left;
     const int steps = steps_of(s);
     const float ca = fmaxf(fabsf(p.c), 1e-30f);  // never 0: a masked score stays -inf when scaled
-    float m = -INFINITY, l = 0.f;  // running maximum (of the raw scores, negated for a negative scale) and sum
+    float m = -INFINITY, l = 0.f;  // running maximum (of the raw scores, negated for a negative scale), and sum of this half
     for (int i = 0; i < steps; ++i) {
       const int tile = tile_of(s, i);
       const bool some = masked(tile);
       wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
       tc_fence_after();
-      uint32_t v[4][32];
+      uint32_t v[2][32];
       if (warp_on) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld_32x32b_x32(tmem + lanes + Sh::kS(s) + b * 32, v[b]);
+        for (int b = 0; b < 2; ++b) tmem_ld_32x32b_x32(tmem + lanes + Sh::kS(s) + half * 64 + b * 32, v[b]);
       }
       if constexpr (DB == 1) {
         // P's columns and O are free again; at 128 channels these scores already waited for that
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       if (warp_on) {
         if (p.c < 0.f) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[b][k] ^= 0x80000000u;
         }
@@ -443,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           const int n = 2 * tile + 1;
           wait_warp(&bar->vready[n % NS], (n / NS) & 1, abort_flag, err);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t w = bar->kept[n % NS][b];
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t w = bar->kept[n % NS][half * 2 + b];
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (!(w >> k & 1u)) v[b][k] = 0xff800000u;
@@ -453,48 +456,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         float mx[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          mx[b] = fmaxf(__uint_as_float(v[b][0]), __uint_as_float(v[b][1]));
+          const uint32_t* u = &v[b >> 1][(b & 1) * 16];
+          mx[b] = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
 #pragma unroll
-          for (int k = 2; k < 32; k += 2) mx[b] = max3(mx[b], __uint_as_float(v[b][k]), __uint_as_float(v[b][k + 1]));
+          for (int k = 2; k < 16; k += 2) mx[b] = max3(mx[b], __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
         }
-        const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float own = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        bar->rowmax[i & 1][s][half][row] = own;
+        tc_fence_before();
+        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // also: both halves hold their scores in registers
+        tc_fence_after();
+        const float tile_max = fmaxf(own, bar->rowmax[i & 1][s][half ^ 1][row]);
         // a row that has seen no key yet takes the tile's maximum; later ones only a clear rise
         const float m_old = m;
         if (m == -INFINITY || (tile_max - m) * ca > kRescaleLog2) m = fmaxf(m, tile_max);
         const float mm = m == -INFINITY ? 0.f : m * ca;
-        if (i > 0) {
+        if (i > 0 && __any_sync(0xffffffffu, m != m_old)) {
           tc_fence_after();
-          if (__any_sync(0xffffffffu, m != m_old)) {
-            const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
-            l *= a;
-            for (int b = 0; b < 4 * DB; ++b) {
-              uint32_t o[16];
-              tmem_ld_x16(tmem + lanes + Sh::kO(s) + b * 16, o);
-              tmem_ld_wait();
+          const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
+          l *= a;
+          for (int b = 0; b < 2 * DB; ++b) {  // each half rescales half of O's columns
+            const uint32_t at = tmem + lanes + Sh::kO(s) + half * 32 * DB + b * 16;
+            uint32_t o[16];
+            tmem_ld_x16(at, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-              tmem_st_x16(tmem + lanes + Sh::kO(s) + b * 16, o);
-            }
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+            tmem_st_x16(at, o);
           }
         }
         const f2 c2 = pack2(ca, ca), m2 = pack2(-mm, -mm);
-        f2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+        f2 sum[2] = {0ull, 0ull};
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int b = 0; b < 2; ++b) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float x, y;
-            unpack2(fma2(pack2(v[h][2 * k], v[h][2 * k + 1]), c2, m2), x, y);
+            unpack2(fma2(pack2(v[b][2 * k], v[b][2 * k + 1]), c2, m2), x, y);
             x = ex2(x);
             y = ex2(y);
-            sum[k & 3] = add2(sum[k & 3], pack2(x, y));
+            sum[k & 1] = add2(sum[k & 1], pack2(x, y));
             w[k] = pack_bf16(x, y);
           }
-          tmem_st_x16(tmem + lanes + Sh::kP(s) + h * 16, w);
+          tmem_st_x16(tmem + lanes + Sh::kP(s) + half * 32 + b * 16, w);
         }
         float x, y;
-        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+        unpack2(add2(sum[0], sum[1]), x, y);
         l += x + y;
         tmem_st_wait();
       }
@@ -505,6 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       wait_warp(&bar->odone[s], (steps - 1) & 1, abort_flag, err);
       tc_fence_after();
     }
+    if (warp_on) {  // the sum of both halves (the buffer of the step before last: its readers are done)
+      bar->rowmax[steps & 1][s][half][row] = l;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      const float other = bar->rowmax[steps & 1][s][half ^ 1][row];
+      l = half ? other + l : l + other;
+    }
     float m2 = l > 0.f ? m * ca : -INFINITY;  // the maximum in base 2; -inf: no key
     if (!(l > 0.f) && !(l == 0.f)) m2 = l;    // NaN scores: carried along
     float* so = reinterpret_cast<float*>(aligned + 2 * Sh::kTileBytes);  // split form: the second stream's state, [column][row]
@@ -512,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const bool merge = !p.pair && nt > 1;
     if (merge) {
       // both streams' last products, and with them every load into the ring, are done before it is reused
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 9, 512;" ::: "memory");
       if (s == 1 && warp_on) {
         so[kCols * kTile + row] = m2;
         so[(kCols + 1) * kTile + row] = l;
 #pragma unroll
-        for (int b = 0; b < 2 * DB; ++b) {
+        for (int b = half * DB; b < half * DB + DB; ++b) {
           uint32_t o[32];
           tmem_ld_32x32b_x32(tmem + lanes + Sh::kO(s) + b * 32, o);
           tmem_ld_wait();
@@ -525,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           for (int k = 0; k < 32; ++k) so[(b * 32 + k) * kTile + row] = __uint_as_float(o[k]);
         }
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 9, 512;" ::: "memory");
     }
     const bool writer = p.pair || s == 0;
     if (warp_on && writer) {
@@ -542,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
       const int64_t at = (int64_t)token * p.Hq + head;
       const float inv = p.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const int64_t rows = (int64_t)p.nq * p.Hq;
-#pragma unroll
-      for (int b = 0; b < 2 * DB; ++b) {
+      for (int b = half * DB; b < half * DB + DB; ++b) {  // each half writes half of the channels
         if (b * 32 >= p.d) break;
         uint32_t o[32];
         if (steps > 0) {
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                                                               pack_bf16(f[k + 4], f[k + 5]), pack_bf16(f[k + 6], f[k + 7]));
         }
       }
-      if (row_on) {
+      if (row_on && half == 0) {
         if (p.splits > 1)
           *reinterpret_cast<float2*>(p.part_ml + (split * rows + at) * 2) = make_float2(m2, l);
         else
@@ -867,8 +880,8 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       warp_arrive(&bar->mready[slot]);
     }
   } else {
-    // ------------------------------------------------------------ P and dS: one thread per fixed row
-    const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+    // ------------------------------------------------------------ P and dS: two threads per fixed row, 32 columns each
+    const int s = warp >> 3, h = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const bool warp_on = (warp & 3) * 32 < left, row_on = row < left;
     const int steps = steps_of(s);
@@ -888,46 +901,43 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       tc_fence_after();
       if (warp_on) {
         const float* st = reinterpret_cast<const float*>(stats + (t % NS) * kStatBytes);
+        uint32_t a[32], b[32], u[16];
+        tmem_ld_32x32b_x32(tmem + lanes + Tm::S(s) + h * 32, a);
+        tmem_ld_32x32b_x32(tmem + lanes + Tm::dP(s) + h * 32, b);
+        tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t a[32], b[32], u[16];
-          tmem_ld_32x32b_x32(tmem + lanes + Tm::S(s) + h * 32, a);
-          tmem_ld_32x32b_x32(tmem + lanes + Tm::dP(s) + h * 32, b);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            ulonglong2 nl = make_ulonglong2(row_lse, row_lse), nd = make_ulonglong2(row_d, row_d);
-            if constexpr (KEYS) {  // a row that takes no part has -lse = -inf there: weight 0
-              nl = *reinterpret_cast<const ulonglong2*>(st + h * 32 + k);
-              nd = *reinterpret_cast<const ulonglong2*>(st + kMove + h * 32 + k);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              float x, y;
-              unpack2(fma2(pack2(a[k + j], a[k + j + 1]), c2, j ? nl.y : nl.x), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              const f2 w = pack2(x, y);
-              const f2 z = mul2(w, add2(pack2(b[k + j], b[k + j + 1]), j ? nd.y : nd.x));
-              if constexpr (KEYS) a[(k + j) / 2] = pack_bf16(x, y);
-              unpack2(z, x, y);
-              u[(k + j) / 2] = pack_bf16(x, y);
-            }
+        for (int k = 0; k < 32; k += 4) {
+          ulonglong2 nl = make_ulonglong2(row_lse, row_lse), nd = make_ulonglong2(row_d, row_d);
+          if constexpr (KEYS) {  // a row that takes no part has -lse = -inf there: weight 0
+            nl = *reinterpret_cast<const ulonglong2*>(st + h * 32 + k);
+            nd = *reinterpret_cast<const ulonglong2*>(st + kMove + h * 32 + k);
           }
-          if constexpr (KEYS) {
-            uint32_t v[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = a[k];
-            tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, v);
-          } else if (partial(t)) {
-            // keys that take no part: weight 0 whatever the products left there
-            if (h == 0) wait_warp(&bar->mready[t % NS], (t / NS) & 1, abort_flag, err);
-            const uint32_t w = bar->kept[t % NS][h];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] &= (w >> (2 * k) & 1u ? 0xffffu : 0u) | (w >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
+          for (int j = 0; j < 4; j += 2) {
+            float x, y;
+            unpack2(fma2(pack2(a[k + j], a[k + j + 1]), c2, j ? nl.y : nl.x), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            const f2 w = pack2(x, y);
+            const f2 z = mul2(w, add2(pack2(b[k + j], b[k + j + 1]), j ? nd.y : nd.x));
+            if constexpr (KEYS) a[(k + j) / 2] = pack_bf16(x, y);
+            unpack2(z, x, y);
+            u[(k + j) / 2] = pack_bf16(x, y);
           }
-          tmem_st_x16(tmem + lanes + Tm::dS(s) + h * 16, u);
         }
+        if constexpr (KEYS) {
+          uint32_t v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = a[k];
+          tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, v);
+        } else if (partial(t)) {
+          // keys that take no part: weight 0 whatever the products left there
+          wait_warp(&bar->mready[t % NS], (t / NS) & 1, abort_flag, err);
+          const uint32_t w = bar->kept[t % NS][h];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] &= (w >> (2 * k) & 1u ? 0xffffu : 0u) | (w >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
+        }
+        tmem_st_x16(tmem + lanes + Tm::dS(s) + h * 16, u);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -935,7 +945,8 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
     }
     if (nt > 0) wait_warp(&bar->fin[1], 0, abort_flag, err);  // both streams' sums are complete
     tc_fence_after();
-    // key pass: warpgroup 0 writes dV and 1 dK; query pass: each half of dQ's channels
+    // key pass: warpgroups 0, 1 write dV and 2, 3 dK, half of the channels each; query pass: a quarter of dQ's each,
+    // at up to 64 channels by the first two
     if (warp_on) {
       const int64_t rows = KEYS ? (int64_t)p.nkv * p.Hkv : (int64_t)p.nq * p.Hq;
       const int64_t at = KEYS ? (int64_t)(f0 + row) * p.Hkv + hk : (int64_t)(f0 + row / p.r) * p.Hq + hk * p.r + row % p.r;
@@ -944,7 +955,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       __nv_bfloat16* out = KEYS ? (s == 0 ? p.dV : p.dK) : p.dQ;
       float* part = KEYS ? (s == 0 ? p.part_v : p.part_k) : p.part_q;
       const int acc = KEYS && s == 0 ? Tm::kAcc1 : Tm::kAcc2;
-      const int b_lo = KEYS ? 0 : s * DB, b_hi = KEYS ? 2 * DB : s * DB + DB;
+      const int b_lo = KEYS ? h * DB : DB == 1 ? (s == 0 ? h : 2) : s * 2 + h, b_hi = KEYS ? h * DB + DB : DB == 1 && s == 1 ? 2 : b_lo + 1;
       for (int b = b_lo; b < b_hi; ++b) {
         if (b * 32 >= p.d) break;
         uint32_t o[32];
@@ -996,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     mbar_init(&bar->ffull, 1);
     for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1), mbar_init(&bar->mready[i], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 4);
+      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 8);
       mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
     }
     mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
