@@ -21,8 +21,9 @@ constexpr int kClipThreads = 256;
 constexpr int kClipCtas = 592;      // 4 per SM on 148 SMs
 constexpr int kClipChunk = 4096;    // values of one tensor per step of a CTA
 constexpr int kClipBatch = 4;       // 16-byte loads in flight per thread
-constexpr int kClipSmall = 64;      // tensors in the small table (2.5 KB of parameters)
-constexpr int kClipLarge = 800;     // tensors in the large one (under the 32,764 bytes a launch may carry)
+constexpr int kClipSmall = 64;      // tensors in the small table (2.2 KB of parameters)
+constexpr int kClipMedium = 256;    // in the medium one (8.5 KB: a launch copies its parameters, ~3 us for the large one)
+constexpr int kClipLarge = 800;     // in the large one (under the 32,764 bytes a launch may carry)
 
 template <int N>
 struct ClipTable {
@@ -299,8 +300,9 @@ int svconv_clip_grads(const svconv_grad* grads, int count, float max_norm, float
   for (int i = 0; i < count; ++i) tensors += grads[i].numel > 0;
   double* part = static_cast<double*>(workspace);
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = tensors <= kClipSmall ? clip_run<kClipSmall>(grads, count, max_norm, norm, part, s)
-                                              : clip_run<kClipLarge>(grads, count, max_norm, norm, part, s);
+  const cudaError_t e = tensors <= kClipSmall    ? clip_run<kClipSmall>(grads, count, max_norm, norm, part, s)
+                        : tensors <= kClipMedium ? clip_run<kClipMedium>(grads, count, max_norm, norm, part, s)
+                                                 : clip_run<kClipLarge>(grads, count, max_norm, norm, part, s);
   return e == cudaSuccess ? SVCONV_OK : SVCONV_ERR_CUDA;
 }
 

@@ -12,9 +12,7 @@ the input's device.
 from __future__ import annotations
 
 import array
-import contextlib
 import ctypes
-import itertools
 import os
 import re
 from typing import Optional, Sequence, Tuple
@@ -405,16 +403,21 @@ def _device_of(t: torch.Tensor) -> int:
     return index
 
 
-def _current(index: int):
-    """Makes device `index` current for a call: launches and device queries go to the current device."""
-    return _SAME_DEVICE if torch.cuda.current_device() == index else torch.cuda.device(index)
+# The current device and raw stream without the Python objects around them, where this torch offers them.
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _raw_stream(index: int, stream) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(index)).cuda_stream
+def _call(name: str, index: int, fn, *args):
+    """fn(*args) with device `index` current (launches and device queries go to the current device)."""
+    if _device_now() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != OK:
+        raise SvconvError(name, rc)
 
 
 def _like(name: str, t: torch.Tensor, shape, dtype, index: int):
@@ -511,11 +514,10 @@ def svconv_cross_attn_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_o
     out = _same("out", out, Q, index)
     lse = _f32("lse", lse, Q.shape[:2], Q, index)
     L, ref = lib(), ctypes.byref(desc)
-    with _current(index):
-        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index)
-        rc = L.svconv_cross_attn_fwd(ref, Q.data_ptr(), K.data_ptr(), V.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                     ws_ptr, ws_bytes, _status(status, index), _raw_stream(index, stream))
-    _check("svconv_cross_attn_fwd", rc)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index)
+    _call("svconv_cross_attn_fwd", index, L.svconv_cross_attn_fwd, ref, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+          out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, _status(status, index),
+          stream.cuda_stream if stream is not None else _stream_now(index))
     return out, lse
 
 
@@ -532,12 +534,10 @@ def svconv_cross_attn_bwd(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V:
     _like("lse", lse, Q.shape[:2], torch.float32, index)
     dQ, dK, dV = _same("dQ", dQ, Q, index), _same("dK", dK, K, index), _same("dV", dV, V, index)
     L, ref = lib(), ctypes.byref(desc)
-    with _current(index):
-        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index)
-        rc = L.svconv_cross_attn_bwd(ref, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
-                                     lse.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws_ptr, ws_bytes,
-                                     _status(status, index), _raw_stream(index, stream))
-    _check("svconv_cross_attn_bwd", rc)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index)
+    _call("svconv_cross_attn_bwd", index, L.svconv_cross_attn_bwd, ref, dO.data_ptr(), Q.data_ptr(), K.data_ptr(),
+          V.data_ptr(), O.data_ptr(), lse.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws_ptr, ws_bytes,
+          _status(status, index), stream.cuda_stream if stream is not None else _stream_now(index))
     return dQ, dK, dV
 
 
@@ -590,9 +590,8 @@ def svconv_qk_norm_rope_fwd(Q: torch.Tensor, K: torch.Tensor, pos_q: torch.Tenso
     index, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
     Yq, Yk = _same("Yq", Yq, Q, index), _same("Yk", Yk, K, index)
     sq.y, sk.y = Yq.data_ptr(), Yk.data_ptr()
-    with _current(index):
-        rc = lib().svconv_qk_norm_rope_fwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), _raw_stream(index, stream))
-    _check("svconv_qk_norm_rope_fwd", rc)
+    _call("svconv_qk_norm_rope_fwd", index, lib().svconv_qk_norm_rope_fwd, *args, float(eps), ctypes.byref(sq),
+          ctypes.byref(sk), stream.cuda_stream if stream is not None else _stream_now(index))
     return Yq, Yk
 
 
@@ -620,15 +619,10 @@ def svconv_qk_norm_rope_bwd(dYq: torch.Tensor, dYk: torch.Tensor, Q: torch.Tenso
         dwq = dwk = None
     sq.dy, sq.dx, sk.dy, sk.dx = dYq.data_ptr(), dQ.data_ptr(), dYk.data_ptr(), dK.data_ptr()
     L = lib()
-    with _current(index):
-        ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_qk_norm_rope_bwd_workspace_size(d), Q, index)
-        rc = L.svconv_qk_norm_rope_bwd(*args, float(eps), ctypes.byref(sq), ctypes.byref(sk), ws_ptr, ws_bytes,
-                                       _raw_stream(index, stream))
-    _check("svconv_qk_norm_rope_bwd", rc)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_qk_norm_rope_bwd_workspace_size(d), Q, index)
+    _call("svconv_qk_norm_rope_bwd", index, L.svconv_qk_norm_rope_bwd, *args, float(eps), ctypes.byref(sq),
+          ctypes.byref(sk), ws_ptr, ws_bytes, stream.cuda_stream if stream is not None else _stream_now(index))
     return dQ, dK, dwq, dwk
-
-
-_GRAD_CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
@@ -643,28 +637,30 @@ def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Op
         raise ValueError("no gradients and no norm tensor: the device is unknown")
     index = _device_of(grads[0] if grads else norm)
     dtypes = [g.dtype for g in grads]
-    if not set(dtypes) <= _GRAD_CODES.keys():
-        raise TypeError(f"fp32 or bf16 gradients are needed, got {set(dtypes)}")
-    every = grads
     sizes = list(map(T.numel, grads))
     src = dst = list(map(T.data_ptr, grads))
+    every = grads
     if out is not None:
         outs = list(out)
         if [o.dtype for o in outs] != dtypes or list(map(T.numel, outs)) != sizes:
             raise ValueError("outputs of the gradients' sizes and types are needed")
         every = grads + outs
         dst = list(map(T.data_ptr, outs))
-    if any(i != index for i in map(T.get_device, every)) or not all(map(T.is_contiguous, every)):
+    if set(map(T.get_device, every)) - {index} or not all(map(T.is_contiguous, every)):
         raise ValueError(f"contiguous tensors on cuda:{index} are needed")
     # svconv_grad records: src, dst, numel, dtype (the low word of the last 8 bytes)
-    flat = array.array("q", itertools.chain.from_iterable(zip(src, dst, sizes, map(_GRAD_CODES.get, dtypes))))
+    flat = array.array("q", bytes(32 * count))
+    flat[0::4], flat[1::4], flat[2::4] = array.array("q", src), array.array("q", dst), array.array("q", sizes)
+    if dtypes.count(torch.float32) != count:
+        if dtypes.count(torch.float32) + dtypes.count(torch.bfloat16) != count:
+            raise TypeError(f"fp32 or bf16 gradients are needed, got {set(dtypes)}")
+        flat[3::4] = array.array("q", [F32 if t is torch.float32 else BF16 for t in dtypes])
     table = flat.buffer_info()[0] if count else None
     norm = _f32("norm", norm, (), grads[0] if grads else norm, index)
     L = lib()
-    with _current(index):
-        ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index)
-        rc = L.svconv_clip_grads(table, count, float(max_norm), norm.data_ptr(), ws_ptr, ws_bytes, _raw_stream(index, stream))
-    _check("svconv_clip_grads", rc)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index)
+    _call("svconv_clip_grads", index, L.svconv_clip_grads, table, count, float(max_norm), norm.data_ptr(), ws_ptr, ws_bytes,
+          stream.cuda_stream if stream is not None else _stream_now(index))
     return norm
 
 
