@@ -186,6 +186,26 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 
+// 32 consecutive values of a row, of which `n` exist (a multiple of 8), by 32-byte stores where the row allows it
+__device__ __forceinline__ void store_row(float* dst, const float (&f)[32], int n) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8)
+    if (k < n) st_global_32(dst + k, reinterpret_cast<const uint32_t*>(f) + k);  // rows of 8 k floats: 32-byte aligned
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&f)[32], int n, bool wide) {
+  uint32_t v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = pack_bf16(f[2 * k], f[2 * k + 1]);
+  if (wide && n >= 32) {
+    st_global_32(dst, v);
+    st_global_32(dst + 16, v + 8);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      if (2 * k < n) *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+  }
+}
+
 // Zero the rows of a tile that must not reach a product (0 x NaN): bit j of drop[w] is row 32 w + j.
 // One warp; a row is 128 contiguous bytes of each 64-channel block whatever the swizzle.
 template <int WORDS>
@@ -233,6 +253,7 @@ struct FwdParams {
   int tokens;       // query tokens of a tile: 128 / r
   int qblocks, splits, pair;
   float c;          // scale * log2(e)
+  int wide;         // rows of O start on 32-byte boundaries
   __nv_bfloat16* O;
   float* lse;
   float* part_o;    // [splits][nq * Hq][d] unnormalised, and
@@ -279,7 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   item /= p.splits;
   const int hk = item % p.Hkv, g = item / p.Hkv;
 
-  if (threadIdx.x == 0) {
+  // Set-up in parallel: the loader makes the barriers and issues the first loads itself, another warp takes
+  // the tensor memory, everyone reads the offsets; one barrier then joins them.
+  if (warp == kLoadWarp && lane == 0) {
     mbar_init(&bar->qfull, 1);
     for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8), mbar_init(&bar->odone[s], 1);
@@ -292,12 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bar->tmem;
   pdl_wait();
-  pdl_trigger();
   int* err = p.status;
 
   int q0, q1, k0, k1;
@@ -314,25 +332,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   auto tile_of = [&](int s, int i) { return p.pair ? i : 2 * i + s; };
   auto masked = [&](int tile) { return p.keep || k0 + (t_lo + tile + 1) * kTile > k1; };
 
-  int loaded = 0;  // K / V tiles whose loads were issued (the loader's count)
+  int loaded = 0;  // K / V tiles whose loads were issued (the loader's count): K, V of each tile in turn
+  auto load_kv = [&] {
+    const int slot = loaded % NS;
+    mbar_arrive_expect_tx(&bar->kvfull[slot], Sh::kTileBytes);
+    for (int b = 0; b < DB; ++b)
+      tma_load_3d(skv + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.tv : &p.tk, &bar->kvfull[slot], b * 64, hk,
+                  k0 + (t_lo + loaded / 2) * kTile);
+    ++loaded;
+  };
+  if (warp == kLoadWarp && lane == 0 && nt > 0) {
+    const uint32_t q_bytes = (uint32_t)(p.tokens * p.r) * 128u * DB;
+    const int nq_tiles = steps_of(1) > 0 && p.pair ? 2 : 1;
+    mbar_arrive_expect_tx(&bar->qfull, q_bytes * nq_tiles);
+    for (int s = 0; s < nq_tiles; ++s)
+      for (int b = 0; b < DB; ++b)
+        tma_load_4d(sq + s * Sh::kTileBytes + b * kBlockBytes, &p.tq, &bar->qfull, b * 64, 0, hk, tok0 + s * p.tokens);
+    while (loaded < min(2 * nt, NS)) load_kv();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // only now may the next kernel's CTAs come and ask for tensor memory: this one has its own
+  pdl_trigger();
+  const uint32_t tmem = bar->tmem;
+
   if (warp == kLoadWarp) {
-    if (lane == 0 && nt > 0) {
-      const uint32_t q_bytes = (uint32_t)(p.tokens * p.r) * 128u * DB;
-      const int nq_tiles = steps_of(1) > 0 && p.pair ? 2 : 1;
-      mbar_arrive_expect_tx(&bar->qfull, q_bytes * nq_tiles);
-      for (int s = 0; s < nq_tiles; ++s)
-        for (int b = 0; b < DB; ++b)
-          tma_load_4d(sq + s * Sh::kTileBytes + b * kBlockBytes, &p.tq, &bar->qfull, b * 64, 0, hk, tok0 + s * p.tokens);
-      for (; loaded < 2 * nt; ++loaded) {  // K, V of each tile in turn
-        const int slot = loaded % NS;
-        if (loaded >= NS) wait_for(&bar->kvempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+    if (lane == 0)
+      while (loaded < 2 * nt) {
+        wait_for(&bar->kvempty[loaded % NS], ((loaded / NS) & 1) ^ 1, abort_flag, err);
         if (*abort_flag) break;
-        mbar_arrive_expect_tx(&bar->kvfull[slot], Sh::kTileBytes);
-        for (int b = 0; b < DB; ++b)
-          tma_load_3d(skv + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.tv : &p.tk, &bar->kvfull[slot], b * 64, hk,
-                      k0 + (t_lo + loaded / 2) * kTile);
+        load_kv();
       }
-    }
   } else if (warp == kScoreWarp) {
     if (nt > 0) {
       const uint32_t e = lane == 0;
@@ -578,19 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           if (merge) f[k] = f[k] * f0 + (f1 != 0.f ? so[(b * 32 + k) * kTile + row] * f1 : 0.f);
           f[k] *= inv;
         }
-        if (p.splits > 1) {
-          float* dst = p.part_o + (split * rows + at) * p.d + b * 32;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            if (b * 32 + k < p.d) *reinterpret_cast<float4*>(dst + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-        } else {
-          __nv_bfloat16* dst = p.O + at * p.d + b * 32;
-#pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            if (b * 32 + k < p.d)
-              *reinterpret_cast<uint4*>(dst + k) = make_uint4(pack_bf16(f[k], f[k + 1]), pack_bf16(f[k + 2], f[k + 3]),
-                                                              pack_bf16(f[k + 4], f[k + 5]), pack_bf16(f[k + 6], f[k + 7]));
-        }
+        if (p.splits > 1) store_row(p.part_o + (split * rows + at) * p.d + b * 32, f, p.d - b * 32);
+        else store_row(p.O + at * p.d + b * 32, f, p.d - b * 32, p.wide);
       }
       if (row_on && half == 0) {
         if (p.splits > 1)
@@ -612,8 +632,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
-// The splits of each (row, head) merged in a fixed order: a warp takes every 8th split, then the
-// warps' states are folded in order.
+// Few splits: a warp merges the splits of a (row, head) one after the other, 4 channels a lane.
+__global__ void __launch_bounds__(256) attn_merge_kernel(const __grid_constant__ FwdParams p) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  int q0, q1, k0, k1;
+  const int flags = group_range(p.q_off, blockIdx.y, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, blockIdx.y, p.nkv, p.max_kv, k0, k1);
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if ((flags & SVCONV_STATUS_BAD_OFFSETS) || i >= (q1 - q0) * p.Hq) return;
+  const int64_t at = (int64_t)q0 * p.Hq + i, rows = (int64_t)p.nq * p.Hq;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int sp = 0; sp < p.splits; ++sp) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (sp * rows + at) * 2);
+    const float4 x = lane * 4 < p.d ? *reinterpret_cast<const float4*>(p.part_o + (sp * rows + at) * p.d + lane * 4) : o;
+    if (ml.y == 0.f) continue;
+    const float top = fmaxf(m, ml.x);
+    const float a = m == -INFINITY ? 0.f : ex2(m - top), b = ex2(ml.x - top);
+    l = l * a + ml.y * b;
+    o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (lane * 4 < p.d)
+    *reinterpret_cast<uint2*>(p.O + at * p.d + lane * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Many splits: a warp takes every 8th split of a (row, head), then the warps' states are folded in order.
 __global__ void __launch_bounds__(256) attn_combine_kernel(const __grid_constant__ FwdParams p) {
   __shared__ float s_ml[8][2], s_o[8][kMaxD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -687,8 +735,10 @@ struct BwdParams {
   const uint8_t* keep;
   int nq, nkv, max_q, max_kv, Hq, Hkv, r, d;
   int qblocks, qsplits, kblocks, ksplits;
-  int q_items;                   // CTAs of the query pass (they come first)
+  int q_items, k_items;          // CTAs of the two passes
+  int keys_first;                // the pass with the longer items comes first
   float c, scale;
+  int wide;                      // rows of the gradients start on 32-byte boundaries
   const float* stat;             // [Hkv][stat_tiles][kStat], see attn_stat_kernel
   int stat_tiles;
   __nv_bfloat16 *dQ, *dK, *dV;
@@ -735,7 +785,6 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
   int* err = p.status;
   const uint32_t sf = base, sm = base + 2 * Sh::kFixedBytes;
   const uint32_t sstat = sm + NS * Sh::kStageBytes;
-  const uint32_t tmem = bar->tmem;
 
   const int blocks = KEYS ? p.kblocks : p.qblocks, splits = KEYS ? p.ksplits : p.qsplits;
   const int block = item % blocks;
@@ -777,34 +826,45 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
   // the statistics of query tile t of the group
   auto stat_of = [&](int t) { return p.stat + ((int64_t)hk * p.stat_tiles + q0 / mtok + g + t) * kStat; };
 
-  int loaded = 0;
-  if (warp == kLoadWarp) {
-    if (lane == 0 && nt > 0) {
-      const CUtensorMap* f[2] = {KEYS ? &p.fk : &p.fq, KEYS ? &p.fv : &p.fdo};
-      const CUtensorMap* m[2] = {KEYS ? &p.mq : &p.mk, KEYS ? &p.mdo : &p.mv};
-      const uint32_t f_bytes = (uint32_t)(KEYS ? kTile : ftok * p.r) * 128u, m_bytes = (uint32_t)(KEYS ? mtok * p.r : kMove) * 128u;
-      mbar_arrive_expect_tx(&bar->ffull, 2 * DB * f_bytes);
-      for (int o = 0; o < 2; ++o)
-        for (int b = 0; b < DB; ++b) {
-          const uint32_t dst = sf + o * Sh::kFixedBytes + b * kBlockBytes;
-          if constexpr (KEYS) tma_load_3d(dst, f[o], &bar->ffull, b * 64, hk, f0);
-          else tma_load_4d(dst, f[o], &bar->ffull, b * 64, 0, hk, f0);
-        }
-      for (; loaded < nt; ++loaded) {
-        const int slot = loaded % NS;
-        if (loaded >= NS) wait_for(&bar->mempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
-        if (*abort_flag) break;
-        mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * m_bytes + (KEYS ? (uint32_t)kStatBytes : 0u));
-        for (int o = 0; o < 2; ++o)
-          for (int b = 0; b < DB; ++b) {
-            const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
-            if constexpr (KEYS) tma_load_4d(dst, m[o], &bar->mfull[slot], b * 64, 0, hk, m0 + loaded * mtok);
-            else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
-          }
-        if constexpr (KEYS)
-          bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
+  int loaded = 0;  // moving tiles whose loads were issued (the loader's count)
+  auto load_moving = [&] {
+    const CUtensorMap* m[2] = {KEYS ? &p.mq : &p.mk, KEYS ? &p.mdo : &p.mv};
+    const int slot = loaded % NS;
+    mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * (uint32_t)(KEYS ? mtok * p.r : kMove) * 128u + (KEYS ? (uint32_t)kStatBytes : 0u));
+    for (int o = 0; o < 2; ++o)
+      for (int b = 0; b < DB; ++b) {
+        const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
+        if constexpr (KEYS) tma_load_4d(dst, m[o], &bar->mfull[slot], b * 64, 0, hk, m0 + loaded * mtok);
+        else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
       }
-    }
+    if constexpr (KEYS) bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
+    ++loaded;
+  };
+  if (warp == kLoadWarp && lane == 0 && nt > 0) {
+    const CUtensorMap* f[2] = {KEYS ? &p.fk : &p.fq, KEYS ? &p.fv : &p.fdo};
+    mbar_arrive_expect_tx(&bar->ffull, 2 * DB * (uint32_t)(KEYS ? kTile : ftok * p.r) * 128u);
+    for (int o = 0; o < 2; ++o)
+      for (int b = 0; b < DB; ++b) {
+        const uint32_t dst = sf + o * Sh::kFixedBytes + b * kBlockBytes;
+        if constexpr (KEYS) tma_load_3d(dst, f[o], &bar->ffull, b * 64, hk, f0);
+        else tma_load_4d(dst, f[o], &bar->ffull, b * 64, 0, hk, f0);
+      }
+    while (loaded < min(nt, NS)) load_moving();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // only now may the next kernel's CTAs come and ask for tensor memory: this one has its own
+  pdl_trigger();
+  const uint32_t tmem = bar->tmem;
+
+  if (warp == kLoadWarp) {
+    if (lane == 0)
+      while (loaded < nt) {
+        wait_for(&bar->mempty[loaded % NS], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+        if (*abort_flag) break;
+        load_moving();
+      }
   } else if (warp == kScoreWarp) {
     if (nt > 0) {
       const uint32_t e = lane == 0;
@@ -974,19 +1034,8 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = live ? __uint_as_float(o[k]) * f : 0.f;
-        if (splits > 1) {
-          float* dst = part + (split * rows + at) * p.d + b * 32;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            if (b * 32 + k < p.d) *reinterpret_cast<float4*>(dst + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        } else {
-          __nv_bfloat16* dst = out + at * p.d + b * 32;
-#pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            if (b * 32 + k < p.d)
-              *reinterpret_cast<uint4*>(dst + k) = make_uint4(pack_bf16(v[k], v[k + 1]), pack_bf16(v[k + 2], v[k + 3]),
-                                                              pack_bf16(v[k + 4], v[k + 5]), pack_bf16(v[k + 6], v[k + 7]));
-        }
+        if (splits > 1) store_row(part + (split * rows + at) * p.d + b * 32, v, p.d - b * 32);
+        else store_row(out + at * p.d + b * 32, v, p.d - b * 32, p.wide);
       }
     }
   }
@@ -1009,8 +1058,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
   uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
   const uint8_t* stats = aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)Sh::kStageBytes;
   BwdBarriers* bar = reinterpret_cast<BwdBarriers*>(aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)(Sh::kStageBytes + kStatBytes));
-  const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) {
+  const int warp = uniform(threadIdx.x >> 5);
+  // set-up as in the forward kernel: the loader's barriers and first loads beside the tensor-memory allocation
+  if (warp == kLoadWarp && (threadIdx.x & 31) == 0) {
     mbar_init(&bar->ffull, 1);
     for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1), mbar_init(&bar->mready[i], 1);
     for (int s = 0; s < 2; ++s) {
@@ -1025,15 +1075,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bar->tmem;
   pdl_wait();
-  pdl_trigger();
-  if ((int)blockIdx.x < p.q_items) bwd_pass<DB, false>(p, blockIdx.x, base, bar, stats);
-  else bwd_pass<DB, true>(p, blockIdx.x - p.q_items, base, bar, stats);
-  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
+  const int first = p.keys_first ? p.k_items : p.q_items, item = (int)blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
+  if (((int)blockIdx.x < first) == (p.keys_first != 0)) bwd_pass<DB, true>(p, item, base, bar, stats);
+  else bwd_pass<DB, false>(p, item, base, bar, stats);
+  if (warp == kSumWarp) tmem_dealloc(bar->tmem, 512);
 }
 
 // -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
@@ -1096,6 +1142,7 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const float* __restrict__
 
 // ---------------------------------------------------------------------------- host side
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Strides of an operand with `heads` heads and `n` rows: the ones that are never used (a single
 // head or row) are replaced, so whatever a caller's view carries there is accepted.
@@ -1167,46 +1214,67 @@ bool make_packed_map(CUtensorMap* m, const void* base, int n, int Hkv, int r, in
 
 int cdiv(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 
-// How a forward call is cut.  Pair form where a group can have more query tokens than one tile holds.  Keys are
-// split where the query blocks leave SMs idle, down to kMinTiles key tiles a split; the counts use fixed numbers
-// (148 SMs), so the workspace size needs no device query.
+// How a forward call is cut: pair or split form, and over how many splits of the keys.  The candidates are
+// compared by the time of whole rounds of CTAs over 148 SMs (a fixed number, so the workspace size needs no device
+// query), with the group lengths known only by their sum and bound.  In units of one key tile for both streams (about
+// 1.1 us): a tile costs 1 in the pair form and 1/2 in the split form, a CTA kFixed besides, and splits their
+// partial results.  Measured with 184 units of 64 key tiles of 128 channels: one split of the pair form 331 us.
 constexpr int kSms = 148, kMinTiles = 4;
+constexpr double kFixed = 3.5, kMerge = 3.0, kMergeBytes = 5.5e6;  // merge: a launch, and bytes a unit
 struct FwdPlan {
   int pair, qblocks, splits;
 };
+double blocks_est(int n, int longest, int G, int rows) {  // blocks of `rows` rows over all groups
+  const double most = (double)G * cdiv(longest, rows);
+  double est = (double)n / rows + 0.5 * G;  // a group's last block is half full
+  if (est < G) est = G;
+  return est < most ? est : most;
+}
 FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
-  FwdPlan f;
-  const int tokens = kTile / (c.Hq / c.Hkv);
-  f.pair = c.max_q > tokens;
-  f.qblocks = f.pair ? cdiv(c.max_q, 2 * tokens) : 1;
-  const long long units = (long long)c.G * c.Hkv * f.qblocks;
-  const int most = cdiv(cdiv(c.max_kv, kTile), kMinTiles);
-  f.splits = units >= kSms ? 1 : (int)(kSms / units);
-  if (f.splits > most) f.splits = most;
-  if (f.splits < 1) f.splits = 1;
-  return f;
+  const int tokens = kTile / (c.Hq / c.Hkv), tiles = cdiv(c.max_kv, kTile);
+  const double merge_bytes = (double)c.nq * c.Hq * c.d * 8.0;
+  FwdPlan best{};
+  double best_t = 0.0;
+  for (int pair = c.max_q > tokens ? 1 : 0; pair >= 0; --pair) {
+    const int rows = tokens * (pair ? 2 : 1);
+    const double units = c.Hkv * blocks_est(c.nq, c.max_q, c.G, rows);
+    for (int s = 1; s == 1 || (s * kMinTiles <= tiles && units * s <= 8.0 * kSms); ++s) {
+      const double rounds = units * s <= kSms ? 1.0 : std::ceil(units * s / kSms);
+      const double t = rounds * ((double)cdiv(tiles, s) * (pair ? 1.0 : 0.5) + kFixed) + (s > 1 ? kMerge + merge_bytes * s / kMergeBytes : 0.0);
+      if (best_t == 0.0 || t < best_t * 0.98) best_t = t, best = FwdPlan{pair, cdiv(c.max_q, rows), s};
+    }
+  }
+  return best;
 }
 
-// The same for the two passes of the backward call.
+// The same for the two passes of the backward call, which share one launch.  A pass whose single item would take
+// more than kLong of an SM's share of all work is split until it does not; the pass with the longer items goes first.
+// In units of one moving tile of the query pass.
+constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kLong = 0.5;
 struct BwdPlan {
-  int qblocks, qsplits, kblocks, ksplits;
+  int qblocks, qsplits, kblocks, ksplits, keys_first;
   int tiles;            // of statistics, for each key head
   size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
   size_t floats() const { return stat + pq + 2 * pk; }
 };
-int bwd_splits(long long units, int tiles) {
-  const int most = cdiv(tiles, 2 * kMinTiles);
-  const int s = units >= kSms ? 1 : (int)(kSms / units);
-  return s > most ? (most < 1 ? 1 : most) : s;
-}
 BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
   BwdPlan b;
-  const int r = c.Hq / c.Hkv;
+  const int r = c.Hq / c.Hkv, G = c.G > 0 ? c.G : 1;
+  const int tq = cdiv(c.max_kv, kMove), tk = cdiv(c.max_q, kMove / r);  // moving tiles of an item of the query / key pass
   b.qblocks = cdiv(c.max_q, kTile / r);
   b.kblocks = cdiv(c.max_kv, kTile);
-  const long long heads = (long long)c.G * c.Hkv;
-  b.qsplits = b.qblocks ? bwd_splits(heads * b.qblocks, cdiv(c.max_kv, kMove)) : 1;
-  b.ksplits = b.kblocks ? bwd_splits(heads * b.kblocks, cdiv(c.max_q, kMove / r)) : 1;
+  const double all = c.Hkv * (blocks_est(c.nq, c.max_q, G, kTile / r) * (cdiv(c.nkv, G * kMove) + kBwdFixed) +
+                              blocks_est(c.nkv, c.max_kv, G, kTile) * (cdiv(c.nq, G * (kMove / r)) * kKeyTile + kBwdFixed));
+  const double share = all / kSms;
+  auto splits = [&](int tiles, double tile) {
+    int s = (int)std::ceil(tiles * tile / (kLong * share));
+    const int most = tiles / (2 * kMinTiles);
+    if (s > most) s = most;
+    return s < 1 ? 1 : s;
+  };
+  b.qsplits = b.qblocks ? splits(tq, 1.0) : 1;
+  b.ksplits = b.kblocks ? splits(tk, kKeyTile) : 1;
+  b.keys_first = (double)tk * kKeyTile / b.ksplits > (double)tq / b.qsplits;
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
   b.tiles = c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
@@ -1270,6 +1338,7 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
   p.qblocks = f.qblocks, p.splits = f.splits, p.pair = f.pair;
   p.c = c.scale * kLog2e;
   p.O = static_cast<__nv_bfloat16*>(O);
+  p.wide = c.d % 16 == 0 && aligned32(O);
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = p.part_o + (size_t)f.splits * c.nq * c.Hq * c.d;
@@ -1281,8 +1350,11 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = c.d <= 64 ? launch_fwd<1>(p, (int)grid, s) : launch_fwd<2>(p, (int)grid, s);
-  if (e == cudaSuccess && f.splits > 1)
+  // a CTA a row hides the chain of many splits; it is wasteful for few (170 us against 20 at 47k rows of 2 splits)
+  if (e == cudaSuccess && f.splits > 8)
     e = launch_pdl(attn_combine_kernel, dim3(c.max_q, c.Hq, c.G), dim3(256), 0, s, p);
+  else if (e == cudaSuccess && f.splits > 1)
+    e = launch_pdl(attn_merge_kernel, dim3((unsigned)(((int64_t)c.max_q * c.Hq + 7) / 8), c.G), dim3(256), 0, s, p);
   return e == cudaSuccess ? SVCONV_OK : SVCONV_ERR_CUDA;
 }
 
@@ -1315,6 +1387,8 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   p.nq = c.nq, p.nkv = c.nkv, p.max_q = c.max_q, p.max_kv = c.max_kv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = r, p.d = c.d;
   p.qblocks = b.qblocks, p.qsplits = b.qsplits, p.kblocks = b.kblocks, p.ksplits = b.ksplits;
   p.q_items = (int)q_items;
+  p.k_items = (int)k_items;
+  p.keys_first = b.keys_first;
   p.c = c.scale * kLog2e;
   p.scale = c.scale;
   p.stat = ws;
@@ -1325,6 +1399,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   p.dQ = static_cast<__nv_bfloat16*>(dQ);
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
+  p.wide = c.d % 16 == 0 && aligned32(dQ) && aligned32(dK) && aligned32(dV);
   p.status = dev_status ? dev_status : device_error_word();
   // a side without rows: its maps only have to be well formed
   const void *q = c.nq ? Q : K, *go = c.nq ? dO : K, *k = c.nkv ? K : Q, *v = c.nkv ? V : Q;
