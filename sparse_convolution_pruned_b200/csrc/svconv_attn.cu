@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "svconv_internal.h"
@@ -97,7 +98,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // nothing branches on the outcome: a call, a result to carry through the loops or one polling lane with a
 // broadcast each cost 10 to 25% of the kernels.  A wait that runs out raises the abort flag, after which every wait
 // returns at once and the loops run to their ends on whatever is there (in bounds; the status word tells).
-__device__ __forceinline__ uint32_t try_wait_many(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ uint32_t try_wait_many(uint32_t bar, uint32_t parity) {
   uint32_t left;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -110,11 +111,11 @@ __device__ __forceinline__ uint32_t try_wait_many(uint64_t* bar, uint32_t parity
       "@q bra ATTN_WAIT;\n\t"
       "ATTN_DONE:\n\t}"
       : "=&r"(left)
-      : "r"(smem_u32(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return left;
 }
-__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
   if (try_wait_many(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
@@ -125,12 +126,38 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
     }
   }
 }
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  wait_for(smem_u32(bar), parity, abort_flag, err);
+}
 // The whole warp waits, and is converged afterwards; mostly the first try succeeds, and a vote is all it takes.
 __device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
   wait_for(bar, parity, abort_flag, err);
   __syncwarp();
 }
+// The same with the barrier at a fixed offset from a shared-memory address that the loop holds anyway: the softmax
+// loops are short of registers, and one for each barrier's address is spilled.
+template <int OFF>
+__device__ __forceinline__ void wait_at(uint32_t at, uint32_t parity, volatile int* abort_flag, int* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1 + %3], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(at), "r"(parity), "n"(OFF)
+      : "memory");
+  if (__all_sync(0xffffffffu, ok != 0)) return;
+  wait_for(at + OFF, parity, abort_flag, err);
+  __syncwarp();
+}
+template <int OFF>
+__device__ __forceinline__ void arrive_at(uint32_t at) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0 + %1];" ::"r"(at), "n"(OFF) : "memory");
+}
+
 // A value that is the same in every lane, told to the compiler as such: what depends on it stays in uniform registers.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -186,24 +213,35 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       : "memory");
 }
 
-// 32 consecutive values of a row, of which `n` exist (a multiple of 8), by 32-byte stores where the row allows it
-__device__ __forceinline__ void store_row(float* dst, const float (&f)[32], int n) {
+// 16 consecutive values of a row, of which `n` exist (a multiple of 8), by 32-byte stores where the row allows it
+__device__ __forceinline__ void store_row(float* dst, const float (&f)[16], int n) {
 #pragma unroll
-  for (int k = 0; k < 32; k += 8)
+  for (int k = 0; k < 16; k += 8)
     if (k < n) st_global_32(dst + k, reinterpret_cast<const uint32_t*>(f) + k);  // rows of 8 k floats: 32-byte aligned
 }
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&f)[32], int n, bool wide) {
-  uint32_t v[16];
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&f)[16], int n, bool wide) {
+  uint32_t v[8];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = pack_bf16(f[2 * k], f[2 * k + 1]);
-  if (wide && n >= 32) {
+  for (int k = 0; k < 8; ++k) v[k] = pack_bf16(f[2 * k], f[2 * k + 1]);
+  if (wide && n >= 16) {
     st_global_32(dst, v);
-    st_global_32(dst + 16, v + 8);
   } else {
 #pragma unroll
-    for (int k = 0; k < 16; k += 4)
+    for (int k = 0; k < 8; k += 4)
       if (2 * k < n) *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
   }
+}
+
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Zero the rows of a tile that must not reach a product (0 x NaN): bit j of drop[w] is row 32 w + j.
@@ -249,9 +287,9 @@ struct FwdParams {
   CUtensorMap tq, tk, tv;
   const int32_t *q_off, *kv_off;
   const uint8_t* keep;
-  int nq, nkv, max_q, max_kv, Hq, Hkv, r, d;
+  int nq, nkv, max_q, max_kv, Hq, Hkv, r, d, G;
   int tokens;       // query tokens of a tile: 128 / r
-  int qblocks, splits, pair;
+  int splits, pair;
   float c;          // scale * log2(e)
   int wide;         // rows of O start on 32-byte boundaries
   __nv_bfloat16* O;
@@ -261,10 +299,76 @@ struct FwdParams {
   int* status;
 };
 
+// One piece of work: a query block of a key head of a group, over one split of the keys.
+struct FwdItem {
+  int nt;                    // key tiles; -1: no more items
+  int steps0, steps1;        // of them, the steps of each stream
+  int tok0, q1;              // first query token of the block, end of the group
+  int k0, k1;                // first key of the split, end of the group
+  int hk, split;
+};
+
+// Walks the items of the whole call in order.  A warp keeps 32 groups at a time, one per lane, so finding an
+// item is a vote and some shuffles, and groups without queries take no item.
+struct FwdCursor {
+  int chunk, base, incl, q0, q1, k0, k1;
+
+  __device__ __forceinline__ void load(const FwdParams& p) {
+    const int g = chunk * 32 + (threadIdx.x & 31);
+    int cnt = 0;
+    q0 = q1 = k0 = k1 = 0;
+    if (g < p.G) {
+      const int f = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
+      const int rows = p.tokens * (p.pair ? 2 : 1);
+      if (!(f & SVCONV_STATUS_BAD_OFFSETS)) cnt = (q1 - q0 + rows - 1) / rows * p.splits * p.Hkv;
+    }
+    incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((int)(threadIdx.x & 31) >= o) incl += v;
+    }
+  }
+  __device__ __forceinline__ bool find(const FwdParams& p, int v, FwdItem& it) {
+    int total = __shfl_sync(0xffffffffu, incl, 31);
+    while (v >= base + total) {
+      base += total;
+      if (++chunk * 32 >= p.G) return false;
+      load(p);
+      total = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int j = __ffs(__ballot_sync(0xffffffffu, v - base < incl)) - 1;
+    const int before = __shfl_sync(0xffffffffu, incl, j > 0 ? j - 1 : 0);
+    int i = v - base - (j > 0 ? before : 0);
+    const int a0 = __shfl_sync(0xffffffffu, q0, j), b0 = __shfl_sync(0xffffffffu, k0, j);
+    it.q1 = __shfl_sync(0xffffffffu, q1, j);
+    it.k1 = __shfl_sync(0xffffffffu, k1, j);
+    // query block fastest, so CTAs that run together share keys in L2
+    const int rows = p.tokens * (p.pair ? 2 : 1), blocks = (it.q1 - a0 + rows - 1) / rows;
+    it.tok0 = a0 + i % blocks * rows;
+    i /= blocks;
+    it.split = i % p.splits;
+    it.hk = i / p.splits;
+    const int tiles = (it.k1 - b0 + kTile - 1) / kTile;
+    const int lo = (int)((int64_t)tiles * it.split / p.splits), hi = (int)((int64_t)tiles * (it.split + 1) / p.splits);
+    it.nt = hi - lo;
+    it.k0 = b0 + lo * kTile;
+    it.steps0 = p.pair ? it.nt : (it.nt + 1) / 2;
+    it.steps1 = p.pair ? (it.tok0 + p.tokens < it.q1 ? it.nt : 0) : it.nt / 2;
+    return true;
+  }
+};
+
+constexpr int kItems = 4;  // items the loader may be ahead
+
 struct FwdBarriers {
-  uint64_t qfull, kvfull[10], kvempty[10], vready[10], sfull[2], sread[2], pfull[2], odone[2], fin[2];
-  uint32_t kept[10][4];  // keys that take part, of the tile whose V lies in this slot
+  uint64_t ifull[kItems], iempty[kItems], qfull[2], qempty[2], kvfull[8], kvempty[8], vready[8];
+  uint64_t sfull[2], sread[2], pfull[2], odone[2], oread[2], fin[2];
+  FwdItem item[kItems];
+  uint32_t kept[8][4];           // keys that take part, of the tile whose V lies in this slot
   float rowmax[2][2][2][kTile];  // [step parity][stream][half of the columns][row], exchanged between the halves
+  float rowsum[2][2][kTile];     // the same for the sums at an item's end
+  float state[2][2][kTile];      // split form: [half][maximum, sum][row] of the second stream
   uint32_t tmem;
   int abort_flag;
 };
@@ -272,41 +376,125 @@ struct FwdBarriers {
 template <int DB>  // 64-channel blocks: 1 (d <= 64) or 2
 struct FwdShape {
   static constexpr int kTileBytes = DB * kBlockBytes;
-  static constexpr int kStages = DB == 1 ? 10 : 4;
-  static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTileBytes + sizeof(FwdBarriers);
+  static constexpr int kQSets = DB == 1 ? 2 : 1;  // looping, the next item's query tiles are loaded ahead
+  static constexpr int kStages = DB == 1 ? 8 : 4;
+  static constexpr size_t kSmem = 1024 + (2 * kQSets + kStages) * (size_t)kTileBytes + sizeof(FwdBarriers);
+  static constexpr int kQ(int set, int s) { return (s * kQSets + set) * kTileBytes; }
+  static constexpr int kExchange = kQSets * kTileBytes;  // split form: the unused second stream's query tiles, 32 KB
   // tensor memory: at 64 channels P has columns of its own, so the next S can be issued before P V; at 128 it takes S's
   static constexpr int kS(int s) { return s * 128; }
   static constexpr int kP(int s) { return DB == 1 ? 256 + s * 64 : s * 128; }
   static constexpr int kO(int s) { return DB == 1 ? 384 + s * 64 : 256 + s * 128; }
 };
 
-template <int DB>
+// The end of an item: the streams' states merged (split form), O divided by the sum and written, or kept as a
+// split's partial result.
+template <int DB, bool PAIR>
+__device__ __forceinline__ void fwd_output(const FwdParams& p, const FwdItem* it, FwdBarriers* bar, uint32_t tmem, float* exchange, int s,
+                                        int half, int row, int steps, float m2, float l) {
+  using Sh = FwdShape<DB>;
+  const int left = min(p.tokens, it->q1 - it->tok0 - (PAIR ? s * p.tokens : 0)) * p.r;
+  const bool warp_on = (row & ~31) < left;
+  const int merge_bar = 9 + half * 2 + (row >> 6);  // named barrier of the two streams' warps of two quarters and this half
+  m2 = l > 0.f ? m2 : -INFINITY;  // no key
+  if (!(l > 0.f) && !(l == 0.f)) m2 = l;    // NaN scores: carried along
+  // split form: the second stream hands its state over, 32 columns of each half at a time
+  float* ex = exchange + half * 32 * kTile + row;
+  const bool merge = !PAIR && it->steps1 > 0;
+  if (merge && s == 1) {
+    bar->state[half][0][row] = m2;
+    bar->state[half][1][row] = l;
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      if (warp_on) {
+#pragma unroll 1
+        for (int c = 0; c < 32; c += 16) {
+          uint32_t o[16];
+          tmem_ld_x16(tmem + Sh::kO(s) + (half * DB + b) * 32 + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) ex[(c + k) * kTile] = __uint_as_float(o[k]);
+        }
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(merge_bar) : "memory");  // written
+      asm volatile("bar.sync %0, 128;" ::"r"(merge_bar) : "memory");  // read
+    }
+  }
+  if (PAIR || s == 0) {
+    const int token = it->tok0 + (PAIR ? s * p.tokens : 0) + row / p.r, head = it->hk * p.r + row % p.r;
+    const int64_t out = (int64_t)token * p.Hq + head, part = it->split * (int64_t)p.nq * p.Hq + out;
+    float f0 = 1.f, f1 = 0.f, inv = 1.f;
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {  // each half writes half of the channels
+      const int c0 = (half * DB + b) * 32;
+      if (merge) asm volatile("bar.sync %0, 128;" ::"r"(merge_bar) : "memory");
+      if (b == 0) {
+        if (merge) {
+          const float m1 = bar->state[half][0][row], l1 = bar->state[half][1][row];
+          const float top = fmaxf(m2, m1);
+          f0 = m2 == -INFINITY ? 0.f : ex2(m2 - top);
+          f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+          l = l * f0 + l1 * f1;
+          m2 = (l == l) ? top : l;
+        }
+        inv = p.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      }
+      if (warp_on) {
+#pragma unroll 1
+        for (int c = c0; c < c0 + 32; c += 16) {
+          uint32_t o[16];
+          if (steps > 0) {
+            tmem_ld_x16(tmem + Sh::kO(s) + c, o);
+            tmem_ld_wait();
+          }
+          float f[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            f[k] = steps > 0 && l != 0.f ? __uint_as_float(o[k]) : 0.f;
+            if (merge) f[k] = f[k] * f0 + (f1 != 0.f ? ex[(c - c0 + k) * kTile] * f1 : 0.f);
+            f[k] *= inv;
+          }
+          if (row < left && c < p.d) {
+            if (p.splits > 1) store_row(p.part_o + part * p.d + c, f, p.d - c);
+            else store_row(p.O + out * p.d + c, f, p.d - c, p.wide);
+          }
+        }
+      }
+      if (merge) asm volatile("bar.sync %0, 128;" ::"r"(merge_bar) : "memory");
+    }
+    if (row < left && half == 0) {
+      if (p.splits > 1) *reinterpret_cast<float2*>(p.part_ml + part * 2) = make_float2(m2, l);
+      else p.lse[out] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
+    }
+  }
+}
+
+// LOOP: a CTA takes every gridDim.x-th item.  Set-up, tensor memory and descriptors are paid once, and the warps
+// run ahead of each other from item to item: the loader by the rings' depth, the products by a tile, so one stream's
+// output and the next item's first tiles overlap (a CTA per item takes 8.7 us for one tile of keys, of which 3 us are
+// set-up and release, and 2 us loads with nothing to do beside them).  Otherwise a CTA takes one item: with many key
+// tiles an item that is the faster form, because in the loop the output's registers spill the softmax's
+// (4096 x 8192 x 8 heads of 64: 111 us against 138; 49152 x 77 x 4 heads: 49 us against 33).
+template <int DB, bool PAIR, bool LOOP>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Sh = FwdShape<DB>;
-  constexpr int NS = Sh::kStages;
+  constexpr int NS = Sh::kStages, NQ = Sh::kQSets;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t sq = base, skv = base + 2 * Sh::kTileBytes;
-  FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(aligned + (2 + NS) * (size_t)Sh::kTileBytes);
+  const uint32_t skv = base + 2 * NQ * Sh::kTileBytes;
+  FwdBarriers* bar = reinterpret_cast<FwdBarriers*>(aligned + (2 * NQ + NS) * (size_t)Sh::kTileBytes);
   volatile int* abort_flag = &bar->abort_flag;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  int* err = p.status;
 
-  // work item: query block fastest, so CTAs that run together share keys in L2
-  int item = blockIdx.x;
-  const int qb = item % p.qblocks;
-  item /= p.qblocks;
-  const int split = item % p.splits;
-  item /= p.splits;
-  const int hk = item % p.Hkv, g = item / p.Hkv;
-
-  // Set-up in parallel: the loader makes the barriers and issues the first loads itself, another warp takes
-  // the tensor memory, everyone reads the offsets; one barrier then joins them.
   if (warp == kLoadWarp && lane == 0) {
-    mbar_init(&bar->qfull, 1);
+    for (int i = 0; i < kItems; ++i) mbar_init(&bar->ifull[i], 1), mbar_init(&bar->iempty[i], kSoftWarps + 3);
     for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8), mbar_init(&bar->odone[s], 1);
-    mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->qfull[s], 1), mbar_init(&bar->qempty[s], 1), mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8);
+      mbar_init(&bar->pfull[s], 8), mbar_init(&bar->odone[s], 1), mbar_init(&bar->oread[s], 8), mbar_init(&bar->fin[s], 1);
+    }
     bar->abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&p.tq), prefetch_tmap(&p.tk), prefetch_tmap(&p.tv);
@@ -315,321 +503,312 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  int* err = p.status;
-
-  int q0, q1, k0, k1;
-  const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
-  if (flags && threadIdx.x == 0 && qb == 0 && split == 0 && hk == 0) atomicOr(p.status, flags);
-  // the first token of each stream's tile, the rows that exist, and this split's key tiles
-  const int tok0 = q0 + qb * p.tokens * (p.pair ? 2 : 1);
-  const bool work = !(flags & SVCONV_STATUS_BAD_OFFSETS) && tok0 < q1;
-  const int tiles = (k1 - k0 + kTile - 1) / kTile;
-  const int t_lo = (int)((int64_t)tiles * split / p.splits), t_hi = work ? (int)((int64_t)tiles * (split + 1) / p.splits) : 0;
-  const int nt = work ? t_hi - t_lo : 0;
-  // tiles of stream s, and the tile of its step i (counted from t_lo)
-  auto steps_of = [&](int s) { return p.pair ? (tok0 + s * p.tokens < q1 ? nt : 0) : (nt + 1 - s) / 2; };
-  auto tile_of = [&](int s, int i) { return p.pair ? i : 2 * i + s; };
-  auto masked = [&](int tile) { return p.keep || k0 + (t_lo + tile + 1) * kTile > k1; };
-
-  int loaded = 0;  // K / V tiles whose loads were issued (the loader's count): K, V of each tile in turn
-  auto load_kv = [&] {
-    const int slot = loaded % NS;
-    mbar_arrive_expect_tx(&bar->kvfull[slot], Sh::kTileBytes);
-    for (int b = 0; b < DB; ++b)
-      tma_load_3d(skv + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.tv : &p.tk, &bar->kvfull[slot], b * 64, hk,
-                  k0 + (t_lo + loaded / 2) * kTile);
-    ++loaded;
-  };
-  if (warp == kLoadWarp && lane == 0 && nt > 0) {
-    const uint32_t q_bytes = (uint32_t)(p.tokens * p.r) * 128u * DB;
-    const int nq_tiles = steps_of(1) > 0 && p.pair ? 2 : 1;
-    mbar_arrive_expect_tx(&bar->qfull, q_bytes * nq_tiles);
-    for (int s = 0; s < nq_tiles; ++s)
-      for (int b = 0; b < DB; ++b)
-        tma_load_4d(sq + s * Sh::kTileBytes + b * kBlockBytes, &p.tq, &bar->qfull, b * 64, 0, hk, tok0 + s * p.tokens);
-    while (loaded < min(2 * nt, NS)) load_kv();
-  }
   tc_fence_before();
-  __syncthreads();
+  // the loader made the barriers itself and needs no tensor memory: it goes ahead
+  if (warp == kLoadWarp) asm volatile("bar.arrive 0, %0;" ::"n"(kThreads) : "memory");
+  else asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
   tc_fence_after();
-  // only now may the next kernel's CTAs come and ask for tensor memory: this one has its own
-  pdl_trigger();
-  const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  if (warp != kLoadWarp) pdl_trigger();  // (after the tensor memory: the next kernel's CTAs may come and ask for theirs)
 
+  int loaded = 0, qloaded = 0;  // K / V tiles and query sets whose loads were issued
   if (warp == kLoadWarp) {
-    if (lane == 0)
-      while (loaded < 2 * nt) {
-        wait_for(&bar->kvempty[loaded % NS], ((loaded / NS) & 1) ^ 1, abort_flag, err);
-        if (*abort_flag) break;
-        load_kv();
+    FwdCursor cur{};
+    cur.load(p);
+    int n = 0;
+    for (int v = blockIdx.x;; v += gridDim.x, ++n) {
+      const int slot = n % kItems;
+      if (n >= kItems) wait_warp(&bar->iempty[slot], ((n / kItems) & 1) ^ 1, abort_flag, err);
+      FwdItem it;
+      it.nt = -1;
+      const bool have = cur.find(p, v, it);
+      if (lane == 0) {
+        bar->item[slot] = it;
+        mbar_arrive(&bar->ifull[slot]);
       }
+      if (!have) break;
+      if (lane == 0)
+        for (int j = 0; j < 2 * it.nt; ++j) {  // K, V of each tile in turn
+          const int kv = loaded % NS;
+          if (loaded >= NS) wait_for(&bar->kvempty[kv], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+          if (*abort_flag) break;
+          mbar_arrive_expect_tx(&bar->kvfull[kv], Sh::kTileBytes);
+          for (int b = 0; b < DB; ++b)
+            tma_load_3d(skv + kv * Sh::kTileBytes + b * kBlockBytes, (j & 1) ? &p.tv : &p.tk, &bar->kvfull[kv], b * 64, it.hk, it.k0 + j / 2 * kTile);
+          ++loaded;
+          if (j == 0) {
+            const int set = qloaded % NQ, tiles = PAIR && it.steps1 > 0 ? 2 : 1;
+            if (qloaded >= NQ) wait_for(&bar->qempty[set], ((qloaded / NQ) & 1) ^ 1, abort_flag, err);
+            if (*abort_flag) break;
+            mbar_arrive_expect_tx(&bar->qfull[set], (uint32_t)(p.tokens * p.r * tiles) * 128u * DB);
+            for (int s = 0; s < tiles; ++s)
+              for (int b = 0; b < DB; ++b)
+                tma_load_4d(base + Sh::kQ(set, s) + b * kBlockBytes, &p.tq, &bar->qfull[set], b * 64, 0, it.hk, it.tok0 + s * p.tokens);
+            ++qloaded;
+          }
+        }
+      if (!LOOP) break;
+    }
+    if (blockIdx.x == 0) {  // every group is looked at once for the status word
+      for (int g = lane; g < p.G; g += 32) {
+        int a0, a1;
+        const int f = group_range(p.q_off, g, p.nq, p.max_q, a0, a1) | group_range(p.kv_off, g, p.nkv, p.max_kv, a0, a1);
+        if (f) atomicOr(err, f);
+      }
+    }
+    pdl_trigger();
   } else if (warp == kScoreWarp) {
-    if (nt > 0) {
-      const uint32_t e = lane == 0;
-      const int ks = (p.d + 15) / 16;
-      const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 0, 0), tm = uniform(tmem);
-      const int steps0 = uniform(steps_of(0)), steps1 = uniform(steps_of(1));
-      const bool pair = p.pair, lone = steps1 == 0;
-      const uint64_t dq = smem_desc_sw128(sq, 16, 1024), dk = smem_desc_sw128(skv, 16, 1024);
-      wait_warp(&bar->qfull, 0, abort_flag, err);
+    const uint32_t e = lane == 0;
+    const int ks = (p.d + 15) / 16;
+    const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 0, 0), tm = uniform(bar->tmem);
+    constexpr bool pair = PAIR;
+    const uint64_t dq = smem_desc_sw128(base, 16, 1024), dk = smem_desc_sw128(skv, 16, 1024);
+    int done0 = 0, done1 = 0, seq = 0, sets = 0;  // steps of each stream, K / V tiles and query sets before this item
+    for (int n = 0;; ++n) {
+      const int at = n % kItems;
+      wait_warp(&bar->ifull[at], (n / kItems) & 1, abort_flag, err);
+      const int nt = uniform(bar->item[at].nt), steps0 = uniform(bar->item[at].steps0), steps1 = uniform(bar->item[at].steps1);
+      warp_arrive(&bar->iempty[at]);
+      if (nt < 0) break;
+      if (nt == 0) {
+        if (LOOP) continue;
+        break;
+      }
+      const bool lone = steps1 == 0;
+      const int set = sets % NQ;
+      wait_warp(&bar->qfull[set], (sets / NQ) & 1, abort_flag, err);
       for (int i = 0; i < steps0; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (i >= (s ? steps1 : steps0)) continue;
-          const int tile = pair ? i : 2 * i + s, n = 2 * tile, slot = n % NS;
+          const int tile = pair ? i : 2 * i + s, k = seq + 2 * tile, slot = k % NS, step = (s ? done1 : done0) + i;
           // S is free once its scores have been read; where P lies in its columns, once P V is done too
-          if (i > 0) wait_warp(DB == 1 ? &bar->sread[s] : &bar->odone[s], (i - 1) & 1, abort_flag, err);
-          if (!pair || s == 0) wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
+          if (step > 0) wait_warp(DB == 1 ? &bar->sread[s] : &bar->odone[s], (step - 1) & 1, abort_flag, err);
+          if (!pair || s == 0) wait_warp(&bar->kvfull[slot], (k / NS) & 1, abort_flag, err);
           tc_fence_after();
-          const uint64_t a0 = dq + (uint64_t)(pair && s ? Sh::kTileBytes >> 4 : 0), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
+          const uint64_t a0 = dq + (uint64_t)((set + (pair && s ? NQ : 0)) * (Sh::kTileBytes >> 4)), b0 = dk + (uint64_t)(slot * (Sh::kTileBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < 4 * DB; ++k) {
-            const uint64_t at = (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2);
-            if (k < ks) mma_ss(tm + Sh::kS(s), a0 + at, b0 + at, idesc, k ? 1u : 0u, e);
+          for (int c = 0; c < 4 * DB; ++c) {
+            const uint64_t off = (uint64_t)((c >> 2) * (kBlockBytes >> 4) + (c & 3) * 2);
+            if (c < ks) mma_ss(tm + Sh::kS(s), a0 + off, b0 + off, idesc, c ? 1u : 0u, e);
           }
           commit_to(&bar->sfull[s], e);
           // the tile's last reader frees it (pair form: the second stream, where it has rows)
           if (!pair || s == 1 || lone) commit_to(&bar->kvempty[slot], e);
         }
-      commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
-      wait_warp(&bar->fin[0], 0, abort_flag, err);
+      commit_to(&bar->qempty[set], e);
+      done0 += steps0, done1 += steps1, seq += 2 * nt, ++sets;
+      if (!LOOP) break;
     }
+    commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
+    wait_warp(&bar->fin[0], 0, abort_flag, err);
   } else if (warp == kSumWarp) {
-    if (nt > 0) {
-      const uint32_t e = lane == 0;
-      const uint32_t idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), tm = uniform(tmem);
-      const int steps0 = uniform(steps_of(0)), steps1 = uniform(steps_of(1));
-      const bool pair = p.pair, lone = steps1 == 0;
-      const uint64_t dv = smem_desc_sw128(skv, kBlockBytes, 1024);
+    const uint32_t e = lane == 0;
+    const uint32_t idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), tm = uniform(bar->tmem);
+    constexpr bool pair = PAIR;
+    const uint64_t dv = smem_desc_sw128(skv, kBlockBytes, 1024);
+    int done0 = 0, done1 = 0, seq = 0, outs0 = 0, outs1 = 0;  // outs: items in which the stream had an output before this one
+    for (int n = 0;; ++n) {
+      const int at = n % kItems;
+      wait_warp(&bar->ifull[at], (n / kItems) & 1, abort_flag, err);
+      const int nt = uniform(bar->item[at].nt), steps0 = uniform(bar->item[at].steps0), steps1 = uniform(bar->item[at].steps1);
+      const int k0 = uniform(bar->item[at].k0), k1 = uniform(bar->item[at].k1);
+      warp_arrive(&bar->iempty[at]);
+      if (nt < 0) break;
+      const bool lone = steps1 == 0;
       for (int i = 0; i < steps0; ++i)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (i >= (s ? steps1 : steps0)) continue;
-          const int tile = pair ? i : 2 * i + s, n = 2 * tile + 1, slot = n % NS;
+          const int tile = pair ? i : 2 * i + s, k = seq + 2 * tile + 1, slot = k % NS, step = (s ? done1 : done0) + i;
           // rows of V behind the group's end or dropped by the mask must be zero: their weights are
-          if (!pair || s == 0) wait_warp(masked(tile) ? &bar->vready[slot] : &bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
+          if (!pair || s == 0)
+            wait_warp(p.keep || k0 + (tile + 1) * kTile > k1 ? &bar->vready[slot] : &bar->kvfull[slot], (k / NS) & 1, abort_flag, err);
           // Where the next scores wait for P V, they go first: O_0, S_0, O_1, S_1 in turn keeps the streams half a
           // period apart, one's softmax under the other's products (left alone they fall into step: 4,700 cycles
           // for both streams' tiles instead of 3,500)
           if constexpr (DB == 2) {
-            if (s == 0 && i > 0 && i < steps1) wait_warp(&bar->sfull[1], i & 1, abort_flag, err);
-            if (s == 1 && i + 1 < steps0) wait_warp(&bar->sfull[0], (i + 1) & 1, abort_flag, err);
+            if (s == 0 && i > 0 && i < steps1) wait_warp(&bar->sfull[1], (done1 + i) & 1, abort_flag, err);
+            if (s == 1 && i + 1 < steps0) wait_warp(&bar->sfull[0], (done0 + i + 1) & 1, abort_flag, err);
           }
-          wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
+          if (i == 0 && (s ? outs1 : outs0) > 0) wait_warp(&bar->oread[s], ((s ? outs1 : outs0) - 1) & 1, abort_flag, err);
+          wait_warp(&bar->pfull[s], step & 1, abort_flag, err);
           tc_fence_after();
           const uint64_t b0 = dv + (uint64_t)(slot * (Sh::kTileBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tm + Sh::kO(s), tm + Sh::kP(s) + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc, (i | k) ? 1u : 0u, e);
+          for (int c = 0; c < kTile / 16; ++c)
+            mma_ts(tm + Sh::kO(s), tm + Sh::kP(s) + c * 8, b0 + (uint64_t)(c * (2048 >> 4)), idesc, (i | c) ? 1u : 0u, e);
           commit_to(&bar->odone[s], e);
           if (!pair || s == 1 || lone) commit_to(&bar->kvempty[slot], e);
         }
-      commit_to(&bar->fin[1], e);
-      wait_warp(&bar->fin[1], 0, abort_flag, err);
+      done0 += steps0, done1 += steps1, seq += 2 * nt, outs0 += steps0 > 0, outs1 += steps1 > 0;
+      if (!LOOP) break;
     }
+    commit_to(&bar->fin[1], e);
+    wait_warp(&bar->fin[1], 0, abort_flag, err);
   } else if (warp == kCheckWarp) {
-    for (int tile = 0; tile < nt; ++tile) {
-      const int n = 2 * tile + 1, slot = n % NS;
-      wait_warp(&bar->kvfull[slot], (n / NS) & 1, abort_flag, err);
-      if (masked(tile)) {
-        uint32_t w[4];
-        kept_words(p.keep, k0 + (t_lo + tile) * kTile, k1, w);
-        if (lane < 4) bar->kept[slot][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+    int seq = 0;
+    for (int n = 0;; ++n) {
+      const int at = n % kItems;
+      wait_warp(&bar->ifull[at], (n / kItems) & 1, abort_flag, err);
+      const int nt = uniform(bar->item[at].nt), k0 = uniform(bar->item[at].k0), k1 = uniform(bar->item[at].k1);
+      warp_arrive(&bar->iempty[at]);
+      if (nt < 0) break;
+      for (int tile = 0; tile < nt; ++tile) {
+        const int k = seq + 2 * tile + 1, slot = k % NS;
+        wait_warp(&bar->kvfull[slot], (k / NS) & 1, abort_flag, err);
+        if (p.keep || k0 + (tile + 1) * kTile > k1) {
+          uint32_t w[4];
+          kept_words(p.keep, k0 + tile * kTile, k1, w);
+          if (lane < 4) bar->kept[slot][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = ~w[i];
-        scrub_rows(skv + slot * Sh::kTileBytes, DB, kBlockBytes, w);
+          for (int i = 0; i < 4; ++i) w[i] = ~w[i];
+          scrub_rows(skv + slot * Sh::kTileBytes, DB, kBlockBytes, w);
+        }
+        warp_arrive(&bar->vready[slot]);
       }
-      warp_arrive(&bar->vready[slot]);
+      seq += 2 * nt;
+      if (!LOOP) break;
     }
   } else {
     // ------------------------------------------------------------ softmax: two threads per row, 64 scores each
     const int s = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int pair_bar = 1 + s * 4 + (warp & 3);  // named barrier of the two warps that hold the same rows
-    const int stok0 = tok0 + (p.pair ? s * p.tokens : 0);
-    const int left = work ? min(p.tokens, q1 - stok0) * p.r : 0;
-    const bool warp_on = (warp & 3) * 32 < left, row_on = row < left;
-    const int steps = steps_of(s);
+    const uint32_t tmem = bar->tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int pair_bar = 1 + s * 4 + (warp & 3);           // named barrier of the two warps that hold the same rows
     const float ca = fmaxf(fabsf(p.c), 1e-30f);  // never 0: a masked score stays -inf when scaled
-    float m = -INFINITY, l = 0.f;  // running maximum (of the raw scores, negated for a negative scale), and sum of this half
-    for (int i = 0; i < steps; ++i) {
-      const int tile = tile_of(s, i);
-      const bool some = masked(tile);
-      wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
-      tc_fence_after();
-      uint32_t v[2][32];
-      if (warp_on) {
+    const uint32_t sb = smem_u32(bar) + s * 8;   // this stream's barriers, at fixed offsets
+    int done = 0, seq = 0;                       // steps of this stream and K / V tiles before this item
+    for (int n = 0;; ++n) {
+      const int at = n % kItems;
+      const FwdItem* it = &bar->item[at];
+      wait_warp(&bar->ifull[at], (n / kItems) & 1, abort_flag, err);
+      if (it->nt < 0) break;
+      const int steps = s ? it->steps1 : it->steps0;
+      const int left = min(p.tokens, it->q1 - it->tok0 - (PAIR ? s * p.tokens : 0)) * p.r;
+      const bool warp_on = (warp & 3) * 32 < left;
+      float m = -INFINITY, l = 0.f;  // running maximum (of the raw scores, negated for a negative scale), and sum of this half
+      for (int i = 0; i < steps; ++i) {
+        const int tile = PAIR ? i : 2 * i + s, step = done + i;
+        const bool some = p.keep || it->k0 + (tile + 1) * kTile > it->k1;
+        wait_at<(int)offsetof(FwdBarriers, sfull)>(sb, step & 1, abort_flag, err);
+        tc_fence_after();
+        uint32_t v[2][32];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) tmem_ld_32x32b_x32(tmem + lanes + Sh::kS(s) + half * 64 + b * 32, v[b]);
-      }
-      if constexpr (DB == 1) {
-        // P's columns and O are free again; at 128 channels these scores already waited for that
-        if (i > 0) wait_warp(&bar->odone[s], (i - 1) & 1, abort_flag, err);
-      }
-      tmem_ld_wait();
-      if constexpr (DB == 1) {
-        // the scores are in registers: the next ones may be computed over them
-        tc_fence_before();
-        warp_arrive(&bar->sread[s]);
-      }
-      if (warp_on) {
-        if (p.c < 0.f) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[b][k] ^= 0x80000000u;
+        for (int b = 0; b < 2; ++b) tmem_ld_32x32b_x32(tmem + Sh::kS(s) + half * 64 + b * 32, v[b]);
+        if constexpr (DB == 1) {
+          // P's columns and O are free again; at 128 channels these scores already waited for that
+          if (step > 0) wait_at<(int)offsetof(FwdBarriers, odone)>(sb, (step - 1) & 1, abort_flag, err);
         }
-        if (some) {
-          const int n = 2 * tile + 1;
-          wait_warp(&bar->vready[n % NS], (n / NS) & 1, abort_flag, err);
+        tmem_ld_wait();
+        if constexpr (DB == 1) {
+          // the scores are in registers: the next ones may be computed over them
+          tc_fence_before();
+          arrive_at<(int)offsetof(FwdBarriers, sread)>(sb);
+        }
+        if (warp_on) {
+          if (p.c < 0.f) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[b][k] ^= 0x80000000u;
+          }
+          if (some) {
+            const int k = seq + 2 * tile + 1;
+            wait_warp(&bar->vready[k % NS], (k / NS) & 1, abort_flag, err);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t w = bar->kept[k % NS][half * 2 + b];
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(w >> k & 1u)) v[b][k] = 0xff800000u;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t* u = &v[b >> 1][(b & 1) * 16];
+            mx[b] = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
+#pragma unroll
+            for (int k = 2; k < 16; k += 2) mx[b] = max3(mx[b], __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+          }
+          const float own = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+          bar->rowmax[step & 1][s][half][row] = own;
+          tc_fence_before();
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // also: both halves hold their scores in registers
+          tc_fence_after();
+          const float tile_max = fmaxf(own, bar->rowmax[step & 1][s][half ^ 1][row]);
+          // a row that has seen no key yet takes the tile's maximum; later ones only a clear rise
+          const float m_old = m;
+          if (m == -INFINITY || (tile_max - m) * ca > kRescaleLog2) m = fmaxf(m, tile_max);
+          const float mm = m == -INFINITY ? 0.f : m * ca;
+          if (i > 0 && __any_sync(0xffffffffu, m != m_old)) {
+            tc_fence_after();
+            const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
+            l *= a;
+#pragma unroll 1
+            for (int b = 0; b < 32 * DB; b += 8) {  // each half rescales half of O's columns; few at a time, beside 64 scores
+              const uint32_t col = tmem + Sh::kO(s) + half * 32 * DB + b;
+              uint32_t o[8];
+              tmem_ld_x8(col, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_st_x8(col, o);
+            }
+          }
+          const f2 c2 = pack2(ca, ca), m2 = pack2(-mm, -mm);
+          f2 sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const uint32_t w = bar->kept[n % NS][half * 2 + b];
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!(w >> k & 1u)) v[b][k] = 0xff800000u;
+            for (int k = 0; k < 16; ++k) {
+              float x, y;
+              unpack2(fma2(pack2(v[b][2 * k], v[b][2 * k + 1]), c2, m2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum[k & 1] = add2(sum[k & 1], pack2(x, y));
+              w[k] = pack_bf16(x, y);
+            }
+            tmem_st_x16(tmem + Sh::kP(s) + half * 32 + b * 16, w);
           }
+          float x, y;
+          unpack2(add2(sum[0], sum[1]), x, y);
+          l += x + y;
+          tmem_st_wait();
         }
-        float mx[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t* u = &v[b >> 1][(b & 1) * 16];
-          mx[b] = fmaxf(__uint_as_float(u[0]), __uint_as_float(u[1]));
-#pragma unroll
-          for (int k = 2; k < 16; k += 2) mx[b] = max3(mx[b], __uint_as_float(u[k]), __uint_as_float(u[k + 1]));
-        }
-        const float own = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-        bar->rowmax[i & 1][s][half][row] = own;
         tc_fence_before();
-        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");  // also: both halves hold their scores in registers
+        arrive_at<(int)offsetof(FwdBarriers, pfull)>(sb);
+      }
+      if (steps > 0) {
+        if (warp_on) {  // the sum of both halves
+          bar->rowsum[s][half][row] = l;
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+          l = bar->rowsum[s][0][row] + bar->rowsum[s][1][row];
+        }
+        wait_at<(int)offsetof(FwdBarriers, odone)>(sb, (done + steps - 1) & 1, abort_flag, err);
         tc_fence_after();
-        const float tile_max = fmaxf(own, bar->rowmax[i & 1][s][half ^ 1][row]);
-        // a row that has seen no key yet takes the tile's maximum; later ones only a clear rise
-        const float m_old = m;
-        if (m == -INFINITY || (tile_max - m) * ca > kRescaleLog2) m = fmaxf(m, tile_max);
-        const float mm = m == -INFINITY ? 0.f : m * ca;
-        if (i > 0 && __any_sync(0xffffffffu, m != m_old)) {
-          tc_fence_after();
-          const float a = m == m_old ? 1.f : ex2(m_old * ca - mm);
-          l *= a;
-          for (int b = 0; b < 2 * DB; ++b) {  // each half rescales half of O's columns
-            const uint32_t at = tmem + lanes + Sh::kO(s) + half * 32 * DB + b * 16;
-            uint32_t o[16];
-            tmem_ld_x16(at, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-            tmem_st_x16(at, o);
-          }
-        }
-        const f2 c2 = pack2(ca, ca), m2 = pack2(-mm, -mm);
-        f2 sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x, y;
-            unpack2(fma2(pack2(v[b][2 * k], v[b][2 * k + 1]), c2, m2), x, y);
-            x = ex2(x);
-            y = ex2(y);
-            sum[k & 1] = add2(sum[k & 1], pack2(x, y));
-            w[k] = pack_bf16(x, y);
-          }
-          tmem_st_x16(tmem + lanes + Sh::kP(s) + half * 32 + b * 16, w);
-        }
-        float x, y;
-        unpack2(add2(sum[0], sum[1]), x, y);
-        l += x + y;
-        tmem_st_wait();
       }
-      tc_fence_before();
-      warp_arrive(&bar->pfull[s]);
-    }
-    if (steps > 0) {
-      wait_warp(&bar->odone[s], (steps - 1) & 1, abort_flag, err);
-      tc_fence_after();
-    }
-    if (warp_on) {  // the sum of both halves (the buffer of the step before last: its readers are done)
-      bar->rowmax[steps & 1][s][half][row] = l;
-      asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-      const float other = bar->rowmax[steps & 1][s][half ^ 1][row];
-      l = half ? other + l : l + other;
-    }
-    float m2 = l > 0.f ? m * ca : -INFINITY;  // the maximum in base 2; -inf: no key
-    if (!(l > 0.f) && !(l == 0.f)) m2 = l;    // NaN scores: carried along
-    float* so = reinterpret_cast<float*>(aligned + 2 * Sh::kTileBytes);  // split form: the second stream's state, [column][row]
-    constexpr int kCols = DB * 64;
-    const bool merge = !p.pair && nt > 1;
-    if (merge) {
-      // both streams' last products, and with them every load into the ring, are done before it is reused
-      asm volatile("bar.sync 9, 512;" ::: "memory");
-      if (s == 1 && warp_on) {
-        so[kCols * kTile + row] = m2;
-        so[(kCols + 1) * kTile + row] = l;
-#pragma unroll
-        for (int b = half * DB; b < half * DB + DB; ++b) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(tmem + lanes + Sh::kO(s) + b * 32, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) so[(b * 32 + k) * kTile + row] = __uint_as_float(o[k]);
-        }
+      fwd_output<DB, PAIR>(p, it, bar, tmem, reinterpret_cast<float*>(aligned + Sh::kExchange), s, half, row, steps, m * ca, l);
+      if (steps > 0) {  // O may be overwritten
+        tc_fence_before();
+        arrive_at<(int)offsetof(FwdBarriers, oread)>(sb);
       }
-      asm volatile("bar.sync 9, 512;" ::: "memory");
-    }
-    const bool writer = p.pair || s == 0;
-    if (warp_on && writer) {
-      float f0 = 1.f, f1 = 0.f;
-      if (merge) {
-        const float m1 = so[kCols * kTile + row], l1 = so[(kCols + 1) * kTile + row];
-        const float top = fmaxf(m2, m1);
-        f0 = m2 == -INFINITY ? 0.f : ex2(m2 - top);
-        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
-        l = l * f0 + l1 * f1;
-        m2 = (l == l) ? top : l;
-      }
-      const int token = stok0 + row / p.r, head = hk * p.r + row % p.r;
-      const int64_t at = (int64_t)token * p.Hq + head;
-      const float inv = p.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      const int64_t rows = (int64_t)p.nq * p.Hq;
-      for (int b = half * DB; b < half * DB + DB; ++b) {  // each half writes half of the channels
-        if (b * 32 >= p.d) break;
-        uint32_t o[32];
-        if (steps > 0) {
-          tmem_ld_32x32b_x32(tmem + lanes + Sh::kO(s) + b * 32, o);
-          tmem_ld_wait();
-        }
-        if (!row_on) continue;
-        float f[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          f[k] = steps > 0 && l != 0.f ? __uint_as_float(o[k]) : 0.f;
-          if (merge) f[k] = f[k] * f0 + (f1 != 0.f ? so[(b * 32 + k) * kTile + row] * f1 : 0.f);
-          f[k] *= inv;
-        }
-        if (p.splits > 1) store_row(p.part_o + (split * rows + at) * p.d + b * 32, f, p.d - b * 32);
-        else store_row(p.O + at * p.d + b * 32, f, p.d - b * 32, p.wide);
-      }
-      if (row_on && half == 0) {
-        if (p.splits > 1)
-          *reinterpret_cast<float2*>(p.part_ml + (split * rows + at) * 2) = make_float2(m2, l);
-        else
-          p.lse[at] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * kLn2;
-      }
+      done += steps, seq += 2 * it->nt;
+      warp_arrive(&bar->iempty[at]);
+      if (!LOOP) break;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (bar->abort_flag && warp == kLoadWarp && lane == 0 && nt > 0) {
+  if (bar->abort_flag && warp == kLoadWarp && lane == 0) {
     // a wait ran out somewhere: let the copies in flight land before the CTA gives its memory back
     volatile int never = 0;
-    mbar_wait(&bar->qfull, 0, &never, err, kDefaultTimeoutNs);
+    for (int i = qloaded > NQ ? qloaded - NQ : 0; i < qloaded; ++i) mbar_wait(&bar->qfull[i % NQ], (i / NQ) & 1, &never, err, kDefaultTimeoutNs);
     for (int i = loaded > NS ? loaded - NS : 0; i < loaded; ++i)
       mbar_wait(&bar->kvfull[i % NS], (i / NS) & 1, &never, err, kDefaultTimeoutNs);
   }
-  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
+  if (warp == kSumWarp) tmem_dealloc(bar->tmem, 512);
 }
 
 // Few splits: a warp merges the splits of a (row, head) one after the other, 4 channels a lane.
@@ -747,7 +926,7 @@ struct BwdParams {
 };
 
 struct BwdBarriers {
-  uint64_t ffull, mfull[8], mempty[8], mready[8], sfull[2], pfull[2], pdone[2], adone[2], fin[2];
+  uint64_t ffull, mfull[8], mempty[8], mready[8], sfull[2], sread[2], pfull[2], pdone[2], adone[2], fin[2];
   uint32_t kept[8][2];  // query pass: keys of the slot's tile that take part
   uint32_t tmem;
   int abort_flag;
@@ -766,6 +945,7 @@ struct BwdShape {
 template <int DB, bool KEYS>
 struct BwdTmem {
   static constexpr bool kShared = DB == 2 && KEYS;
+  static constexpr bool kEarly = !kShared;
   static constexpr int kStride = DB == 1 ? 192 : KEYS ? 128 : 160;
   static constexpr int S(int s) { return s * kStride; }
   static constexpr int dP(int s) { return s * kStride + 64; }
@@ -785,6 +965,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
   int* err = p.status;
   const uint32_t sf = base, sm = base + 2 * Sh::kFixedBytes;
   const uint32_t sstat = sm + NS * Sh::kStageBytes;
+  const uint32_t tmem = bar->tmem;
 
   const int blocks = KEYS ? p.kblocks : p.qblocks, splits = KEYS ? p.ksplits : p.qsplits;
   const int block = item % blocks;
@@ -826,45 +1007,34 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
   // the statistics of query tile t of the group
   auto stat_of = [&](int t) { return p.stat + ((int64_t)hk * p.stat_tiles + q0 / mtok + g + t) * kStat; };
 
-  int loaded = 0;  // moving tiles whose loads were issued (the loader's count)
-  auto load_moving = [&] {
-    const CUtensorMap* m[2] = {KEYS ? &p.mq : &p.mk, KEYS ? &p.mdo : &p.mv};
-    const int slot = loaded % NS;
-    mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * (uint32_t)(KEYS ? mtok * p.r : kMove) * 128u + (KEYS ? (uint32_t)kStatBytes : 0u));
-    for (int o = 0; o < 2; ++o)
-      for (int b = 0; b < DB; ++b) {
-        const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
-        if constexpr (KEYS) tma_load_4d(dst, m[o], &bar->mfull[slot], b * 64, 0, hk, m0 + loaded * mtok);
-        else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
-      }
-    if constexpr (KEYS) bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
-    ++loaded;
-  };
-  if (warp == kLoadWarp && lane == 0 && nt > 0) {
-    const CUtensorMap* f[2] = {KEYS ? &p.fk : &p.fq, KEYS ? &p.fv : &p.fdo};
-    mbar_arrive_expect_tx(&bar->ffull, 2 * DB * (uint32_t)(KEYS ? kTile : ftok * p.r) * 128u);
-    for (int o = 0; o < 2; ++o)
-      for (int b = 0; b < DB; ++b) {
-        const uint32_t dst = sf + o * Sh::kFixedBytes + b * kBlockBytes;
-        if constexpr (KEYS) tma_load_3d(dst, f[o], &bar->ffull, b * 64, hk, f0);
-        else tma_load_4d(dst, f[o], &bar->ffull, b * 64, 0, hk, f0);
-      }
-    while (loaded < min(nt, NS)) load_moving();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  // only now may the next kernel's CTAs come and ask for tensor memory: this one has its own
-  pdl_trigger();
-  const uint32_t tmem = bar->tmem;
-
+  int loaded = 0;
   if (warp == kLoadWarp) {
-    if (lane == 0)
-      while (loaded < nt) {
-        wait_for(&bar->mempty[loaded % NS], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+    if (lane == 0 && nt > 0) {
+      const CUtensorMap* f[2] = {KEYS ? &p.fk : &p.fq, KEYS ? &p.fv : &p.fdo};
+      const CUtensorMap* m[2] = {KEYS ? &p.mq : &p.mk, KEYS ? &p.mdo : &p.mv};
+      const uint32_t f_bytes = (uint32_t)(KEYS ? kTile : ftok * p.r) * 128u, m_bytes = (uint32_t)(KEYS ? mtok * p.r : kMove) * 128u;
+      mbar_arrive_expect_tx(&bar->ffull, 2 * DB * f_bytes);
+      for (int o = 0; o < 2; ++o)
+        for (int b = 0; b < DB; ++b) {
+          const uint32_t dst = sf + o * Sh::kFixedBytes + b * kBlockBytes;
+          if constexpr (KEYS) tma_load_3d(dst, f[o], &bar->ffull, b * 64, hk, f0);
+          else tma_load_4d(dst, f[o], &bar->ffull, b * 64, 0, hk, f0);
+        }
+      for (; loaded < nt; ++loaded) {
+        const int slot = loaded % NS;
+        if (loaded >= NS) wait_for(&bar->mempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
         if (*abort_flag) break;
-        load_moving();
+        mbar_arrive_expect_tx(&bar->mfull[slot], 2 * DB * m_bytes + (KEYS ? (uint32_t)kStatBytes : 0u));
+        for (int o = 0; o < 2; ++o)
+          for (int b = 0; b < DB; ++b) {
+            const uint32_t dst = sm + slot * Sh::kStageBytes + o * Sh::kMoveBytes + b * kMoveBlock;
+            if constexpr (KEYS) tma_load_4d(dst, m[o], &bar->mfull[slot], b * 64, 0, hk, m0 + loaded * mtok);
+            else tma_load_3d(dst, m[o], &bar->mfull[slot], b * 64, hk, m0 + loaded * kMove);
+          }
+        if constexpr (KEYS)
+          bulk_copy_g2s(sstat + slot * kStatBytes, stat_of(t_lo + loaded), kStatBytes, &bar->mfull[slot]);
       }
+    }
   } else if (warp == kScoreWarp) {
     if (nt > 0) {
       const uint32_t e = lane == 0;
@@ -890,7 +1060,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
           wait_warp(partial(t) ? &bar->mready[slot] : &bar->mfull[slot], (t / NS) & 1, abort_flag, err);
           // the scores' columns are free once they have been read; where P and dS lie in them, once the sums
           // that read those are done
-          if (t0 > 0) wait_warp(Tm::kShared ? &bar->pdone[s] : &bar->pfull[s], ph, abort_flag, err);
+          if (t0 > 0) wait_warp(Tm::kShared ? &bar->pdone[s] : Tm::kEarly ? &bar->sread[s] : &bar->pfull[s], ph, abort_flag, err);
           tc_fence_after();
           scores(0, slot, tm + Tm::S(s));
           if (Tm::kShared && t0 > 0) {
@@ -966,12 +1136,19 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
       if (i > 0) wait_warp(&bar->adone[s], (i - 1) & 1, abort_flag, err);  // P and dS are free again
       tc_fence_after();
+      uint32_t a[32], b[32];
       if (warp_on) {
-        const float* st = reinterpret_cast<const float*>(stats + (t % NS) * kStatBytes);
-        uint32_t a[32], b[32], u[16];
         tmem_ld_32x32b_x32(tmem + lanes + Tm::S(s) + h * 32, a);
         tmem_ld_32x32b_x32(tmem + lanes + Tm::dP(s) + h * 32, b);
-        tmem_ld_wait();
+      }
+      tmem_ld_wait();
+      if constexpr (Tm::kEarly) {  // the scores are in registers: the next ones may be computed over them
+        tc_fence_before();
+        warp_arrive(&bar->sread[s]);
+      }
+      if (warp_on) {
+        const float* st = reinterpret_cast<const float*>(stats + (t % NS) * kStatBytes);
+        uint32_t u[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
           ulonglong2 nl = make_ulonglong2(row_lse, row_lse), nd = make_ulonglong2(row_d, row_d);
@@ -1023,19 +1200,20 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       float* part = KEYS ? (s == 0 ? p.part_v : p.part_k) : p.part_q;
       const int acc = KEYS && s == 0 ? Tm::kAcc1 : Tm::kAcc2;
       const int b_lo = KEYS ? h * DB : DB == 1 ? (s == 0 ? h : 2) : s * 2 + h, b_hi = KEYS ? h * DB + DB : DB == 1 && s == 1 ? 2 : b_lo + 1;
-      for (int b = b_lo; b < b_hi; ++b) {
-        if (b * 32 >= p.d) break;
-        uint32_t o[32];
+#pragma unroll 1
+      for (int c = b_lo * 32; c < b_hi * 32; c += 16) {
+        if (c >= p.d) break;
+        uint32_t o[16];
         if (nt > 0) {
-          tmem_ld_32x32b_x32(tmem + lanes + acc + b * 32, o);
+          tmem_ld_x16(tmem + lanes + acc + c, o);
           tmem_ld_wait();
         }
         if (!row_on) continue;
-        float v[32];
+        float v[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = live ? __uint_as_float(o[k]) * f : 0.f;
-        if (splits > 1) store_row(part + (split * rows + at) * p.d + b * 32, v, p.d - b * 32);
-        else store_row(out + at * p.d + b * 32, v, p.d - b * 32, p.wide);
+        for (int k = 0; k < 16; ++k) v[k] = live ? __uint_as_float(o[k]) * f : 0.f;
+        if (splits > 1) store_row(part + (split * rows + at) * p.d + c, v, p.d - c);
+        else store_row(out + at * p.d + c, v, p.d - c, p.wide);
       }
     }
   }
@@ -1058,13 +1236,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
   uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
   const uint8_t* stats = aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)Sh::kStageBytes;
   BwdBarriers* bar = reinterpret_cast<BwdBarriers*>(aligned + 2 * Sh::kFixedBytes + Sh::kStages * (size_t)(Sh::kStageBytes + kStatBytes));
-  const int warp = uniform(threadIdx.x >> 5);
-  // set-up as in the forward kernel: the loader's barriers and first loads beside the tensor-memory allocation
-  if (warp == kLoadWarp && (threadIdx.x & 31) == 0) {
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
     mbar_init(&bar->ffull, 1);
     for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1), mbar_init(&bar->mready[i], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->pfull[s], 8);
+      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8);
       mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
     }
     mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
@@ -1075,11 +1252,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
   pdl_wait();
+  pdl_trigger();
   const int first = p.keys_first ? p.k_items : p.q_items, item = (int)blockIdx.x < first ? blockIdx.x : blockIdx.x - first;
   if (((int)blockIdx.x < first) == (p.keys_first != 0)) bwd_pass<DB, true>(p, item, base, bar, stats);
   else bwd_pass<DB, false>(p, item, base, bar, stats);
-  if (warp == kSumWarp) tmem_dealloc(bar->tmem, 512);
+  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
 // -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
@@ -1220,6 +1402,10 @@ int cdiv(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 // 1.1 us): a tile costs 1 in the pair form and 1/2 in the split form, a CTA kFixed besides, and splits their
 // partial results.  Measured with 184 units of 64 key tiles of 128 channels: one split of the pair form 331 us.
 constexpr int kSms = 148, kMinTiles = 4;
+// Up to so many key tiles an item, CTAs loop over items at up to 64 channels (24,576 queries x 4 heads: 1 tile 27 us a
+// CTA an item and 21 us looping, 4 tiles 42 and 39, 8 tiles 64 and 64).  At 128 channels looping loses at every length
+// (29 and 33 us at 1 tile): its query tiles cannot be loaded ahead.
+constexpr int kLoopTiles = 6;
 constexpr double kFixed = 3.5, kMerge = 3.0, kMergeBytes = 5.5e6;  // merge: a launch, and bytes a unit
 struct FwdPlan {
   int pair, qblocks, splits;
@@ -1247,34 +1433,71 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
   return best;
 }
 
-// The same for the two passes of the backward call, which share one launch.  A pass whose single item would take
-// more than kLong of an SM's share of all work is split until it does not; the pass with the longer items goes first.
-// In units of one moving tile of the query pass.
-constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kLong = 0.5;
+// The same for the two passes of the backward call, which share one launch: CTAs take the items of the pass with
+// the longer ones first, then the other's, as SMs come free.  Splits are tried around the number that keeps an item under
+// half an SM's share of all work, by that schedule's end plus the cost of the partial results.  In units of one
+// moving tile of the query pass (about 0.6 us).
+constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kBwdMerge = 5.0, kBwdMergeBytes = 3.0e6;
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits, keys_first;
   int tiles;            // of statistics, for each key head
   size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
   size_t floats() const { return stat + pq + 2 * pk; }
 };
+// When kSms machines that take na items of la, then nb of lb, as they come free, are done.
+double schedule_end(double na, double la, double nb, double lb) {
+  if (na + nb > 30.0 * kSms) return (na * la + nb * lb) / kSms + (la > lb ? la : lb) * 0.5;
+  struct {
+    double t, n;
+  } free[80];  // machines by the time they come free, earliest first
+  int cnt = 1;
+  free[0] = {0.0, (double)kSms};
+  double end = 0.0;
+  for (int k = 0; k < 2; ++k) {
+    double n = k ? nb : na;
+    const double l = k ? lb : la;
+    while (n > 0.0) {
+      const double take = n < free[0].n ? n : free[0].n, t = free[0].t + l;
+      n -= take;
+      if (t > end) end = t;
+      if (take < free[0].n) {
+        free[0].n -= take;
+      } else {
+        --cnt;
+        for (int i = 0; i < cnt; ++i) free[i] = free[i + 1];
+      }
+      int i = cnt++;
+      while (i > 0 && free[i - 1].t > t) free[i] = free[i - 1], --i;
+      free[i] = {t, take};
+    }
+  }
+  return end;
+}
 BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
   BwdPlan b;
   const int r = c.Hq / c.Hkv, G = c.G > 0 ? c.G : 1;
   const int tq = cdiv(c.max_kv, kMove), tk = cdiv(c.max_q, kMove / r);  // moving tiles of an item of the query / key pass
   b.qblocks = cdiv(c.max_q, kTile / r);
   b.kblocks = cdiv(c.max_kv, kTile);
-  const double all = c.Hkv * (blocks_est(c.nq, c.max_q, G, kTile / r) * (cdiv(c.nkv, G * kMove) + kBwdFixed) +
-                              blocks_est(c.nkv, c.max_kv, G, kTile) * (cdiv(c.nq, G * (kMove / r)) * kKeyTile + kBwdFixed));
-  const double share = all / kSms;
-  auto splits = [&](int tiles, double tile) {
-    int s = (int)std::ceil(tiles * tile / (kLong * share));
-    const int most = tiles / (2 * kMinTiles);
-    if (s > most) s = most;
-    return s < 1 ? 1 : s;
-  };
-  b.qsplits = b.qblocks ? splits(tq, 1.0) : 1;
-  b.ksplits = b.kblocks ? splits(tk, kKeyTile) : 1;
-  b.keys_first = (double)tk * kKeyTile / b.ksplits > (double)tq / b.qsplits;
+  const double nqb = b.qblocks ? c.Hkv * blocks_est(c.nq, c.max_q, G, kTile / r) : 0.0;
+  const double nkb = b.kblocks ? c.Hkv * blocks_est(c.nkv, c.max_kv, G, kTile) : 0.0;
+  const double share = (nqb * (cdiv(c.nkv, G * kMove) + kBwdFixed) + nkb * (cdiv(c.nq, G * (kMove / r)) * kKeyTile + kBwdFixed)) / kSms;
+  const double bq = (double)c.nq * c.Hq * c.d * 8.0 / kBwdMergeBytes, bk = 2.0 * c.nkv * c.Hkv * c.d * 8.0 / kBwdMergeBytes;
+  auto start = [&](int tiles, double tile) { return share > 0.0 ? (int)std::ceil(tiles * tile / (0.5 * share)) : 1; };
+  const int mq = tq / (2 * kMinTiles), mk = tk / (2 * kMinTiles);  // most splits
+  const int sq0 = start(tq, 1.0), sk0 = start(tk, kKeyTile);
+  double best = 0.0;
+  for (int i = -3; i < 2; ++i)
+    for (int j = -3; j < 2; ++j) {
+      int sq = i == -3 ? 1 : sq0 + i, sk = j == -3 ? 1 : sk0 + j;
+      sq = sq > mq ? mq : sq, sk = sk > mk ? mk : sk;
+      sq = sq < 1 ? 1 : sq, sk = sk < 1 ? 1 : sk;
+      const double lq = (double)tq / sq + kBwdFixed, lk = (double)tk * kKeyTile / sk + kBwdFixed;
+      const bool kf = lk > lq;
+      const double t = (kf ? schedule_end(nkb * sk, lk, nqb * sq, lq) : schedule_end(nqb * sq, lq, nkb * sk, lk)) +
+                       (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? 2 * kBwdMerge + bk * sk : 0.0);
+      if (best == 0.0 || t < best) best = t, b.qsplits = sq, b.ksplits = sk, b.keys_first = kf;
+    }
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
   b.tiles = c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
@@ -1291,10 +1514,17 @@ cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t s) {
 }
 
 template <int DB>
-cudaError_t launch_fwd(const FwdParams& p, int grid, cudaStream_t s) {
-  static int done[64];
-  cudaError_t e = ensure_smem_attr(attn_fwd_kernel<DB>, FwdShape<DB>::kSmem, done);
-  return e == cudaSuccess ? launch_pdl(attn_fwd_kernel<DB>, dim3(grid), dim3(kThreads), FwdShape<DB>::kSmem, s, p) : e;
+cudaError_t launch_fwd(const FwdParams& p, int items, int tiles, cudaStream_t s) {
+  static int done[4][64];
+  const int ctas = sm_count();
+  bool loop = false;
+  auto kernel = p.pair ? attn_fwd_kernel<DB, true, false> : attn_fwd_kernel<DB, false, false>;
+  if constexpr (DB == 1) {
+    loop = items > ctas && tiles <= kLoopTiles;
+    if (loop) kernel = p.pair ? attn_fwd_kernel<DB, true, true> : attn_fwd_kernel<DB, false, true>;
+  }
+  cudaError_t e = ensure_smem_attr(kernel, FwdShape<DB>::kSmem, done[2 * p.pair + loop]);
+  return e == cudaSuccess ? launch_pdl(kernel, dim3(loop ? ctas : items), dim3(kThreads), FwdShape<DB>::kSmem, s, p) : e;
 }
 
 }  // namespace
@@ -1335,7 +1565,7 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
   p.q_off = c.q_off, p.kv_off = c.kv_off, p.keep = c.kv_keep;
   p.nq = c.nq, p.nkv = c.nkv, p.max_q = c.max_q, p.max_kv = c.max_kv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = c.Hq / c.Hkv, p.d = c.d;
   p.tokens = kTile / p.r;
-  p.qblocks = f.qblocks, p.splits = f.splits, p.pair = f.pair;
+  p.G = c.G, p.splits = f.splits, p.pair = f.pair;
   p.c = c.scale * kLog2e;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.wide = c.d % 16 == 0 && aligned32(O);
@@ -1349,7 +1579,8 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
       !make_rows_map(&p.tv, c.nkv ? V : Q, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kTile))
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = c.d <= 64 ? launch_fwd<1>(p, (int)grid, s) : launch_fwd<2>(p, (int)grid, s);
+  const int tiles = cdiv(cdiv(c.max_kv, kTile), f.splits);
+  cudaError_t e = c.d <= 64 ? launch_fwd<1>(p, (int)grid, tiles, s) : launch_fwd<2>(p, (int)grid, tiles, s);
   // a CTA a row hides the chain of many splits; it is wasteful for few (170 us against 20 at 47k rows of 2 splits)
   if (e == cudaSuccess && f.splits > 8)
     e = launch_pdl(attn_combine_kernel, dim3(c.max_q, c.Hq, c.G), dim3(256), 0, s, p);
