@@ -2,6 +2,7 @@
 
 ``svconv`` is the Python binding of the C-ABI CUDA library (loaded on first
 use; it raises if the library is missing or no CUDA device is present).
-``workloads`` holds the seeded synthetic input generators.
+``workloads`` holds the seeded synthetic input generators, ``recombine`` the
+normed, rotated cross-attention of two token streams with its gradients.
 """
-__all__ = ["svconv", "workloads"]
+__all__ = ["svconv", "workloads", "recombine"]

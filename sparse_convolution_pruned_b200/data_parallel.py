@@ -54,3 +54,15 @@ def allreduce_grads(grads, group=None):
     if dist.is_initialized() and dist.get_world_size(group) > 1:
         dist.all_reduce(grads, op=dist.ReduceOp.SUM, group=group)
     return grads
+
+
+def allreduce_and_clip(grads, max_norm: float, group=None):
+    """Sum each gradient tensor over the ranks, then clip all of them, in place, by their global norm
+    (svconv_clip_grads on the device).  Every rank holds the same sums, so every rank takes the same norm
+    and the same factor.  Returns the norm before clipping (fp32 scalar tensor)."""
+    from . import svconv
+
+    grads = list(grads)
+    for g in grads:
+        allreduce_grads(g, group)
+    return svconv.svconv_clip_grads(grads, max_norm)

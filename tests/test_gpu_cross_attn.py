@@ -172,6 +172,49 @@ def test_scales(sv, scale):
     check(x, run_both(sv, x, scale=scale), scale, f"scale {scale}")
 
 
+def test_strided_queries(sv):
+    """Q as heads 1.. of a wider tensor; K and V as every other head of one."""
+    x = make(6, (140, 3), (260, 31), 4, 2, 64)
+    wide = torch.zeros((x["Q"].shape[0], 5, 64), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:] = x["Q"]
+    kv = torch.zeros((x["K"].shape[0], 4, 64), dtype=torch.bfloat16, device="cuda")
+    kv[:, 0::2], kv[:, 1::2] = x["K"], x["V"]
+    want = run_both(sv, x)
+    y = dict(x, Q=wide[:, 1:], K=kv[:, 0::2], V=kv[:, 1::2])
+    got = run_both(sv, y)
+    for k in want:
+        assert torch.equal(want[k], got[k]), k
+
+
+def test_rows_beyond_32_bit_offsets(sv):
+    """17 million keys of 128 channels: element offsets pass 2^31.  The mask keeps the last 900 and a few early ones."""
+    n, d = 17_000_000, 128
+    x = make(30, (5,), (900,), 1, 1, d)
+    at = torch.cat([torch.arange(0, 300, device="cuda"), torch.arange(n - 600, n, device="cuda")])
+    big = {k: torch.zeros((n, 1, d), dtype=torch.bfloat16, device="cuda") for k in ("K", "V")}
+    for k in big:
+        big[k][at] = x[k]
+    keep = torch.zeros((n,), dtype=torch.uint8, device="cuda")
+    keep[at] = 1
+    y = dict(x, K=big["K"], V=big["V"], keep=keep, kv_off=offsets((n,)), max_kv=n)
+    args = dict(max_q=5, max_kv=n, kv_keep=keep)
+    O, lse = sv.svconv_cross_attn_fwd(y["Q"], y["K"], y["V"], y["q_off"], y["kv_off"], **args)
+    dQ, dK, dV = sv.svconv_cross_attn_bwd(y["dO"], y["Q"], y["K"], y["V"], O, lse, y["q_off"], y["kv_off"], **args)
+    torch.cuda.synchronize()
+    check(x, {"O": O, "lse": lse, "dQ": dQ, "dK": dK[at], "dV": dV[at]}, d ** -0.5, "17M keys")
+    assert not dK[300:n - 600].any() and not dV[300:n - 600].any()
+
+
+def test_many_groups(sv):
+    """More groups than a warp has lanes, lengths from 0 on, some groups empty on either side."""
+    rng = np.random.default_rng(5)
+    q_lens, kv_lens = tuple(int(v) for v in rng.integers(0, 9, 150)), tuple(int(v) for v in rng.integers(0, 200, 150))
+    x = make(31, q_lens, kv_lens, 4, 2, 64, keep=0.8, gap=2)
+    check(x, run_both(sv, x), 0.125, "150 groups")
+    x = make(32, (300,) * 40, (90,) * 40, 2, 1, 64)  # many items of one key tile each
+    check(x, run_both(sv, x), 0.125, "40 groups")
+
+
 def test_large_scores_saturate_without_overflow(sv):
     """Scores of several hundred: the softmax collapses onto single keys."""
     x = make(8, (130,), (400,), 2, 2, 64, scale=60.0)

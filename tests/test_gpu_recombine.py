@@ -1,0 +1,142 @@
+"""The operators in a run together: norm and rotation, cross-attention, their gradients, and the clipping of all
+of them with a convolution's, against the same chain in 64 bits by autograd.
+
+Bounds are norms: each bf16 tensor that passes from one operator to the next is off by u / sqrt(3) of its size at
+most on average (u = 2^-8, a rounding is uniform within half a step), and so are the matrix operands P and dS.  A
+gradient here passes at most eight such roundings (Yq, Yk, P, O, dS, dY, and its own, one of them twice), each at
+most doubled by the terms it is a difference of: 16 u / sqrt(3) of its norm, 0.036.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_convolution_pruned_b200 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+REL = 16 * 2.0 ** -8 / math.sqrt(3)
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_convolution_pruned_b200 import build, svconv
+    build.build()
+    return svconv
+
+
+def rel(a, b):
+    return float((a.double() - b).norm() / b.norm())
+
+
+def chain64(x, rot, q_lens, kv_lens, scale):
+    """O by the formulas in fp64, differentiable."""
+    def normed(t, pos, w):
+        u = t * torch.rsqrt(t.square().mean(-1, keepdim=True) + rot.eps) * w
+        axis = torch.tensor([a for a, m in enumerate(rot.axis_pairs) for _ in range(m)], device="cuda")
+        ang = (pos.double()[:, axis] * rot.freq)[:, None]
+        p = len(rot.freq)
+        a, b = u[..., :p], u[..., p:2 * p]
+        return torch.cat([a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos(), u[..., 2 * p:]], -1)
+    Yq, Yk = normed(x["Q"], x["pos_q"], x["wq"]), normed(x["K"], x["pos_k"], x["wk"])
+    r = Yq.shape[1] // Yk.shape[1]
+    out, q0, k0 = [], 0, 0
+    for a, b in zip(q_lens, kv_lens):
+        q, k, v = Yq[q0:q0 + a].transpose(0, 1), Yk[k0:k0 + b].transpose(0, 1), x["V"][k0:k0 + b].transpose(0, 1)
+        k, v = k.repeat_interleave(r, 0), v.repeat_interleave(r, 0)
+        out.append((torch.softmax(scale * q @ k.transpose(1, 2), -1) @ v).transpose(0, 1))
+        q0, k0 = q0 + a, k0 + b
+    return torch.cat(out)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 4, 4), (128, 4, 2)])
+def test_chain_forward_backward_clip(sv, d, Hq, Hkv):
+    from sparse_convolution_pruned_b200 import data_parallel, recombine as rc
+    w = wl.custom_conv(seed=5, T=12, H=16, W=16, keep_frac=0.3, Cin=64, Cout=64, dtype="bf16")
+    dev = lambda a, dt=None: (torch.from_numpy(np.ascontiguousarray(a)).to(dt) if dt else torch.from_numpy(np.ascontiguousarray(a))).cuda()
+    coords, off = dev(w.coords), w.frame_off.astype(np.int64)
+    # the keys are the sparse tokens, four frames to a group; the queries a few auxiliary tokens of each group
+    kv_lens = [int(off[t + 4] - off[t]) for t in range(0, 12, 4)]
+    q_lens = [3, 17, 150]
+    nq, nk = sum(q_lens), sum(kv_lens)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(d)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = {"Q": rnd(nq, Hq, d).bfloat16(), "K": rnd(nk, Hkv, d).bfloat16(), "V": rnd(nk, Hkv, d).bfloat16(),
+         "wq": 1 + 0.2 * rnd(d), "wk": 1 + 0.2 * rnd(d), "pos_k": coords,
+         "pos_q": torch.randint(0, 12, (nq, 3), generator=gen, device="cuda", dtype=torch.int32)}
+    dO = rnd(nq, Hq, d).bfloat16()
+    cum = lambda v: torch.tensor(np.concatenate([[0], np.cumsum(v)]), dtype=torch.int32, device="cuda")
+    groups = rc.Groups(cum(q_lens), cum(kv_lens), max(q_lens), max(kv_lens))
+    pairs = (d // 8, d // 8, d // 8)
+    rot = rc.Rotation(rc.axis_frequencies(pairs, 100.0), pairs)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        nbr, _ = sv.svconv_build_index(coords, dev_off, w.T, w.H, w.W)
+        dX, dW, db = sv.svconv_bwd(dY, X, nbr, Wt)
+        O, saved = rc.recombine_fwd(x["Q"], x["K"], x["V"], x["pos_q"], x["pos_k"], groups, rot, wq=x["wq"], wk=x["wk"], status=st)
+        g = rc.recombine_bwd(dO, saved, groups, rot, status=st)
+        return O, (dW, db) + g
+
+    dev_off, X, Wt, dY = dev(w.frame_off), dev(w.X, torch.bfloat16), dev(w.Wt, torch.bfloat16), dev(w.dY, torch.bfloat16)
+    O, grads = step()
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and sv.svconv_read_error_word() == 0
+
+    ref = {k: (v.double().requires_grad_(True) if v.is_floating_point() else v) for k, v in x.items()}
+    O64 = chain64(ref, rot, q_lens, kv_lens, d ** -0.5)
+    O64.backward(dO.double())
+    assert rel(O, O64.detach()) <= REL
+    names = ("dQ", "dK", "dV", "dwq", "dwk")
+    for name, got, leaf in zip(names, grads[2:], ("Q", "K", "V", "wq", "wk")):
+        assert rel(got, ref[leaf].grad) <= REL, name
+
+    # clipping of everything together
+    total = math.sqrt(sum(float((g.double() ** 2).sum()) for g in grads))
+    keep = [g.clone() for g in grads]
+    norm = data_parallel.allreduce_and_clip(grads, total / 5)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - total) <= 2.0 ** -22 * total
+    for g, k in zip(grads, keep):
+        u = torch.finfo(g.dtype).eps / 2
+        want = k.double() / 5
+        assert ((g.double() - want).abs() <= (u + 2.0 ** -20) * want.abs() + 1e-38).all()
+
+    # the whole step captured, replayed after its inputs changed
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        O2, grads2 = step()
+        norm2 = data_parallel.allreduce_and_clip(grads2, total / 5)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(O2, O) and torch.equal(norm2, norm)
+    for a, b in zip(grads2, grads):
+        assert torch.equal(a, b)
+    x["Q"].mul_(2.0)  # the norm takes a factor out again: O must not move beyond rounding
+    gr.replay()
+    torch.cuda.synchronize()
+    assert rel(O2, O64.detach()) <= REL
+
+
+def test_rotation_sees_relative_positions_only(sv):
+    """Moving every position of both streams by the same offset leaves O where it was, within rounding."""
+    from sparse_convolution_pruned_b200 import recombine as rc
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    Q, K, V = rnd(40, 2, 64).bfloat16(), rnd(500, 2, 64).bfloat16(), rnd(500, 2, 64).bfloat16()
+    pq = torch.randint(0, 500, (40,), generator=gen, device="cuda", dtype=torch.int32)
+    pk = torch.arange(500, dtype=torch.int32, device="cuda")
+    off = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    groups, rot = rc.Groups(off(40), off(500), 40, 500), rc.Rotation(rc.axis_frequencies((32,)), (32,))
+    a, _ = rc.recombine_fwd(Q, K, V, pq, pk, groups, rot)
+    b, _ = rc.recombine_fwd(Q, K, V, pq + 1_000_000, pk + 1_000_000, groups, rot)
+    torch.cuda.synchronize()
+    assert rel(a, b.double()) <= REL
