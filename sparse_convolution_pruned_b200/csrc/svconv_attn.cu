@@ -473,8 +473,7 @@ __device__ __forceinline__ void fwd_output(const FwdParams& p, const FwdItem* it
 // run ahead of each other from item to item: the loader by the rings' depth, the products by a tile, so one stream's
 // output and the next item's first tiles overlap (a CTA per item takes 8.7 us for one tile of keys, of which 3 us are
 // set-up and release, and 2 us loads with nothing to do beside them).  Otherwise a CTA takes one item: with many key
-// tiles an item that is the faster form, because in the loop the output's registers spill the softmax's
-// (4096 x 8192 x 8 heads of 64: 111 us against 138; 49152 x 77 x 4 heads: 49 us against 33).
+// tiles an item that is the faster form, because in the loop the output's registers spill the softmax's (kLoopTiles).
 template <int DB, bool PAIR, bool LOOP>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Sh = FwdShape<DB>;
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             wait_warp(p.keep || k0 + (tile + 1) * kTile > k1 ? &bar->vready[slot] : &bar->kvfull[slot], (k / NS) & 1, abort_flag, err);
           // Where the next scores wait for P V, they go first: O_0, S_0, O_1, S_1 in turn keeps the streams half a
           // period apart, one's softmax under the other's products (left alone they fall into step: 4,700 cycles
-          // for both streams' tiles instead of 3,500)
+          // for both streams' tiles instead of 4,000)
           if constexpr (DB == 2) {
             if (s == 0 && i > 0 && i < steps1) wait_warp(&bar->sfull[1], (done1 + i) & 1, abort_flag, err);
             if (s == 1 && i + 1 < steps0) wait_warp(&bar->sfull[0], (done0 + i + 1) & 1, abort_flag, err);
@@ -1400,12 +1399,12 @@ int cdiv(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 // compared by the time of whole rounds of CTAs over 148 SMs (a fixed number, so the workspace size needs no device
 // query), with the group lengths known only by their sum and bound.  In units of one key tile for both streams (about
 // 1.1 us): a tile costs 1 in the pair form and 1/2 in the split form, a CTA kFixed besides, and splits their
-// partial results.  Measured with 184 units of 64 key tiles of 128 channels: one split of the pair form 331 us.
+// partial results.  Measured with 184 units of 64 key tiles of 128 channels: one split of the pair form 308 us.
 constexpr int kSms = 148, kMinTiles = 4;
-// Up to so many key tiles an item, CTAs loop over items at up to 64 channels (24,576 queries x 4 heads: 1 tile 27 us a
-// CTA an item and 21 us looping, 4 tiles 42 and 39, 8 tiles 64 and 64).  At 128 channels looping loses at every length
-// (29 and 33 us at 1 tile): its query tiles cannot be loaded ahead.
-constexpr int kLoopTiles = 6;
+// Up to so many key tiles an item, CTAs loop over items.  24,576 queries x 4 heads of 64: 1 tile 26.7 us a CTA an item
+// and 20.6 us looping, 2 tiles 29.2 and 24.7, 4 tiles 37 and 37, 8 tiles 55 and 59; heads of 128, whose query tiles
+// cannot be loaded ahead: 1 tile 26.7 and 23.9, 2 tiles 32.9 and 30.9, 3 tiles 39.0 and 37.9.
+constexpr int kLoopTiles = 3;
 constexpr double kFixed = 3.5, kMerge = 3.0, kMergeBytes = 5.5e6;  // merge: a launch, and bytes a unit
 struct FwdPlan {
   int pair, qblocks, splits;
@@ -1517,12 +1516,9 @@ template <int DB>
 cudaError_t launch_fwd(const FwdParams& p, int items, int tiles, cudaStream_t s) {
   static int done[4][64];
   const int ctas = sm_count();
-  bool loop = false;
-  auto kernel = p.pair ? attn_fwd_kernel<DB, true, false> : attn_fwd_kernel<DB, false, false>;
-  if constexpr (DB == 1) {
-    loop = items > ctas && tiles <= kLoopTiles;
-    if (loop) kernel = p.pair ? attn_fwd_kernel<DB, true, true> : attn_fwd_kernel<DB, false, true>;
-  }
+  const bool loop = items > ctas && tiles <= kLoopTiles;
+  auto kernel = p.pair ? (loop ? attn_fwd_kernel<DB, true, true> : attn_fwd_kernel<DB, true, false>)
+                       : (loop ? attn_fwd_kernel<DB, false, true> : attn_fwd_kernel<DB, false, false>);
   cudaError_t e = ensure_smem_attr(kernel, FwdShape<DB>::kSmem, done[2 * p.pair + loop]);
   return e == cudaSuccess ? launch_pdl(kernel, dim3(loop ? ctas : items), dim3(kThreads), FwdShape<DB>::kSmem, s, p) : e;
 }

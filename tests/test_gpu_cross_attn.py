@@ -213,6 +213,10 @@ def test_many_groups(sv):
     check(x, run_both(sv, x), 0.125, "150 groups")
     x = make(32, (300,) * 40, (90,) * 40, 2, 1, 64)  # many items of one key tile each
     check(x, run_both(sv, x), 0.125, "40 groups")
+    rng = np.random.default_rng(6)
+    for d in (64, 128):  # more items than SMs, of none to three key tiles
+        x = make(33, (300,) * 80, tuple(int(v) for v in rng.integers(0, 380, 80)), 4, 4, d, keep=0.9)
+        check(x, run_both(sv, x), d ** -0.5, f"80 groups of {d} channels")
 
 
 def test_large_scores_saturate_without_overflow(sv):
