@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
   if (warp == kLoadWarp && lane == 0) {
     for (int i = 0; i < kItems; ++i) mbar_init(&bar->ifull[i], 1), mbar_init(&bar->iempty[i], kSoftWarps + 3);
-    for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1), mbar_init(&bar->vready[i], 1);
+    // K and V tiles alternate, so V's slots are the odd ones: the check warp has to be done with those too
+    for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 1 + (i & 1)), mbar_init(&bar->vready[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->qfull[s], 1), mbar_init(&bar->qempty[s], 1), mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8);
       mbar_init(&bar->pfull[s], 8), mbar_init(&bar->odone[s], 1), mbar_init(&bar->oread[s], 8), mbar_init(&bar->fin[s], 1);
@@ -665,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
           scrub_rows(skv + slot * Sh::kTileBytes, DB, kBlockBytes, w);
         }
         warp_arrive(&bar->vready[slot]);
+        warp_arrive(&bar->kvempty[slot]);
       }
       seq += 2 * nt;
       if (!LOOP) break;
@@ -1114,6 +1116,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
         scrub_rows(sm + slot * Sh::kStageBytes, 2 * DB, kMoveBlock, w);
       }
       warp_arrive(&bar->mready[slot]);
+      warp_arrive(&bar->mempty[slot]);  // the products' last reader is the other arrival
     }
   } else {
     // ------------------------------------------------------------ P and dS: two threads per fixed row, 32 columns each
@@ -1238,7 +1241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bar->ffull, 1);
-    for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 1), mbar_init(&bar->mready[i], 1);
+    for (int i = 0; i < Sh::kStages; ++i) mbar_init(&bar->mfull[i], 1), mbar_init(&bar->mempty[i], 2), mbar_init(&bar->mready[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8);
       mbar_init(&bar->pdone[s], 1), mbar_init(&bar->adone[s], 1);
@@ -1325,6 +1328,9 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const float* __restrict__
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// Rows, and items of a launch: a row, block or item behind the last one still has a 32-bit number.
+constexpr int kMaxRows = 0x7fff0000;
+
 // Strides of an operand with `heads` heads and `n` rows: the ones that are never used (a single
 // head or row) are replaced, so whatever a caller's view carries there is accepted.
 bool fix_strides(int64_t& row, int64_t& head, int n, int heads, int d) {
@@ -1337,6 +1343,7 @@ int check_desc(const svconv_cross_attn_desc* c, svconv_cross_attn_desc& o) {
   if (!c) return SVCONV_ERR_NULL;
   o = *c;
   if (o.nq < 0 || o.nkv < 0 || o.G < 0 || o.max_q < 0 || o.max_kv < 0) return SVCONV_ERR_SIZE;
+  if (o.nq > kMaxRows || o.nkv > kMaxRows) return SVCONV_ERR_SIZE;
   if (o.Hq < 1 || o.Hkv < 1 || o.Hq > 65535 || o.G > 65535) return SVCONV_ERR_SIZE;
   if (o.d < 8 || o.d > kMaxD || o.d % 8 != 0 || o.Hq % o.Hkv != 0 || o.Hq / o.Hkv > kMove) return SVCONV_ERR_UNSUPPORTED;
   if (!std::isfinite(o.scale)) return SVCONV_ERR_SIZE;
@@ -1556,7 +1563,7 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
   if ((rc = check_device())) return rc;
   const FwdPlan f = plan_fwd(c);
   const long long grid = (long long)c.G * c.Hkv * f.qblocks * f.splits;
-  if (grid > 0x7fffffffLL) return SVCONV_ERR_SIZE;
+  if (grid > kMaxRows) return SVCONV_ERR_SIZE;
   FwdParams p{};
   p.q_off = c.q_off, p.kv_off = c.kv_off, p.keep = c.kv_keep;
   p.nq = c.nq, p.nkv = c.nkv, p.max_q = c.max_q, p.max_kv = c.max_kv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = c.Hq / c.Hkv, p.d = c.d;
@@ -1607,7 +1614,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   int lanes = 1;
   while (lanes < c.d / 8) lanes *= 2;
   const long long stat_grid = (long long)cdiv(c.max_q, kMove / r) * c.Hkv;
-  if (q_items + k_items > 0x7fffffffLL || stat_grid > 0x7fffffffLL) return SVCONV_ERR_SIZE;
+  if (q_items + k_items > kMaxRows || stat_grid > kMaxRows) return SVCONV_ERR_SIZE;
   float* ws = static_cast<float*>(workspace);
   BwdParams p{};
   p.q_off = c.q_off, p.kv_off = c.kv_off, p.keep = c.kv_keep;

@@ -36,7 +36,8 @@ def bwd(L, d, dO=A, Q=A, K=A, V=A, O=A, lse=A, dQ=A, dK=A, dV=A, ws=A, n=1 << 40
 
 
 @pytest.mark.parametrize("bad,code", [
-    (dict(nq=-1), SIZE), (dict(nkv=-1), SIZE), (dict(G=-1), SIZE), (dict(max_q=-1), SIZE), (dict(max_kv=-1), SIZE),
+    (dict(nq=-1), SIZE), (dict(nkv=-1), SIZE), (dict(nq=2**31 - 1), SIZE), (dict(nkv=2**31 - 1), SIZE), (dict(G=-1), SIZE), (dict(max_q=-1), SIZE), (dict(max_kv=-1), SIZE),
+    (dict(Hq=2**16, Hkv=2**16), SIZE), (dict(G=2**16), SIZE),
     (dict(Hq=0), SIZE), (dict(Hkv=0), SIZE), (dict(scale=math.nan), SIZE), (dict(scale=math.inf), SIZE),
     (dict(d=0), UNSUP), (dict(d=60), UNSUP), (dict(d=136), UNSUP), (dict(Hq=5), UNSUP), (dict(Hq=130, Hkv=2), UNSUP),
     (dict(q_off=None), NULL), (dict(kv_off=None), NULL),
