@@ -63,7 +63,8 @@ class Saved:
 
 def recombine_fwd(Q, K, V, pos_q, pos_k, groups: Groups, rotation: Rotation, *, wq=None, wk=None, kv_keep=None,
                   scale: Optional[float] = None, status=None, stream=None):
-    """Q [nq, Hq, d], K and V [nkv, Hkv, d] bf16 -> (O [nq, Hq, d] bf16, Saved)."""
+    """Q [nq, Hq, d], K and V [nkv, Hkv, d] bf16 -> (O [nq, Hq, d] bf16, Saved).  O's rows of no group are left
+    as they were allocated."""
     Yq, Yk = svconv.svconv_qk_norm_rope_fwd(Q, K, pos_q, pos_k, rotation.freq, wq=wq, wk=wk, eps=rotation.eps,
                                             layout=rotation.layout, axis_pairs=rotation.axis_pairs, stream=stream)
     O, lse = svconv.svconv_cross_attn_fwd(Yq, Yk, V, groups.q_off, groups.kv_off, max_q=groups.max_q,
@@ -73,11 +74,16 @@ def recombine_fwd(Q, K, V, pos_q, pos_k, groups: Groups, rotation: Rotation, *, 
 
 
 def recombine_bwd(dO, saved: Saved, groups: Groups, rotation: Rotation, *, status=None, stream=None):
-    """(dQ, dK, dV bf16, dwq, dwk fp32 [d]) of recombine_fwd.  Every row must belong to a group: a row of
-    none has no gradient written, and would enter dwq or dwk with whatever memory held."""
+    """(dQ, dK, dV bf16, dwq, dwk fp32 [d]) of recombine_fwd.  Rows of no group (a padded batch's) get zero
+    gradients; they and left-out keys add nothing to dwq and dwk as long as what they hold is finite."""
+    grads = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (saved.Yq, saved.Yk, saved.V)]
+    with torch.cuda.stream(stream):
+        for t in grads:
+            t.zero_()
     dYq, dYk, dV = svconv.svconv_cross_attn_bwd(dO, saved.Yq, saved.Yk, saved.V, saved.O, saved.lse, groups.q_off,
                                                 groups.kv_off, max_q=groups.max_q, max_kv=groups.max_kv,
-                                                scale=saved.scale, kv_keep=saved.kv_keep, status=status, stream=stream)
+                                                scale=saved.scale, kv_keep=saved.kv_keep, dQ=grads[0], dK=grads[1],
+                                                dV=grads[2], status=status, stream=stream)
     dQ, dK, dwq, dwk = svconv.svconv_qk_norm_rope_bwd(
         dYq, dYk, saved.Q, saved.K, saved.pos_q, saved.pos_k, rotation.freq, wq=saved.wq, wk=saved.wk, eps=rotation.eps,
         layout=rotation.layout, axis_pairs=rotation.axis_pairs, dQ=dYq, dK=dYk, stream=stream)

@@ -442,12 +442,15 @@ def _f32(name: str, t: Optional[torch.Tensor], shape, like: torch.Tensor, index:
     return t
 
 
-def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int):
-    """(tensor to keep until the launch, its address, its bytes)."""
+def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int, stream=None):
+    """(tensor to keep until the launch, its address, its bytes).  One allocated here, for a call on another
+    stream than the current one, is not given out again before that stream is done with it."""
     if ws is None:
         if not need:
             return None, None, 0
         ws = like.new_empty((need,), dtype=torch.uint8)
+        if stream is not None:
+            ws.record_stream(stream)
     elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{index} is needed")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -469,6 +472,8 @@ def _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep) -> Tuple[i
     nkv, Hkv, dk = kshape = K.shape
     if dk != d or V.shape != kshape:
         raise ValueError(f"Q {tuple(Q.shape)}, K {tuple(K.shape)} and V {tuple(V.shape)} do not fit together")
+    if (nq | nkv) >> 31:
+        raise ValueError("the library counts rows in 32 bits")
     strides = []
     for name, t in (("Q", Q), ("K", K), ("V", V)):
         if t.dtype is not torch.bfloat16:
@@ -514,7 +519,7 @@ def svconv_cross_attn_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_o
     out = _same("out", out, Q, index)
     lse = _f32("lse", lse, Q.shape[:2], Q, index)
     L, ref = lib(), ctypes.byref(desc)
-    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index, stream)
     _call("svconv_cross_attn_fwd", index, L.svconv_cross_attn_fwd, ref, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
           out.data_ptr(), lse.data_ptr(), ws_ptr, ws_bytes, _status(status, index),
           stream.cuda_stream if stream is not None else _stream_now(index))
@@ -534,7 +539,7 @@ def svconv_cross_attn_bwd(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V:
     _like("lse", lse, Q.shape[:2], torch.float32, index)
     dQ, dK, dV = _same("dQ", dQ, Q, index), _same("dK", dK, K, index), _same("dV", dV, V, index)
     L, ref = lib(), ctypes.byref(desc)
-    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index, stream)
     _call("svconv_cross_attn_bwd", index, L.svconv_cross_attn_bwd, ref, dO.data_ptr(), Q.data_ptr(), K.data_ptr(),
           V.data_ptr(), O.data_ptr(), lse.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws_ptr, ws_bytes,
           _status(status, index), stream.cuda_stream if stream is not None else _stream_now(index))
@@ -565,6 +570,8 @@ def _qk_common(Q, K, pq, pk, freq, layout, axis_pairs, wq, wk):
         if x.dim() != 3 or x.shape[2] != d or x.dtype is not dtype or x.get_device() != index:
             raise ValueError(f"{name}: [rows, heads, {d}] {dtype} on cuda:{index} is needed")
         n, H, _ = x.shape
+        if n >> 31:
+            raise ValueError("the library counts rows in 32 bits")
         row, head, one = x.stride()
         if n and ((d > 1 and one != 1) or (H > 1 and head != d)):
             raise ValueError(f"{name}: contiguous heads are needed (rows may be strided)")
@@ -619,7 +626,7 @@ def svconv_qk_norm_rope_bwd(dYq: torch.Tensor, dYk: torch.Tensor, Q: torch.Tenso
         dwq = dwk = None
     sq.dy, sq.dx, sk.dy, sk.dx = dYq.data_ptr(), dQ.data_ptr(), dYk.data_ptr(), dK.data_ptr()
     L = lib()
-    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_qk_norm_rope_bwd_workspace_size(d), Q, index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_qk_norm_rope_bwd_workspace_size(d), Q, index, stream)
     _call("svconv_qk_norm_rope_bwd", index, L.svconv_qk_norm_rope_bwd, *args, float(eps), ctypes.byref(sq),
           ctypes.byref(sk), ws_ptr, ws_bytes, stream.cuda_stream if stream is not None else _stream_now(index))
     return dQ, dK, dwq, dwk
@@ -658,7 +665,7 @@ def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Op
     table = flat.buffer_info()[0] if count else None
     norm = _f32("norm", norm, (), grads[0] if grads else norm, index)
     L = lib()
-    ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index, stream)
     _call("svconv_clip_grads", index, L.svconv_clip_grads, table, count, float(max_norm), norm.data_ptr(), ws_ptr, ws_bytes,
           stream.cuda_stream if stream is not None else _stream_now(index))
     return norm

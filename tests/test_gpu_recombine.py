@@ -140,3 +140,71 @@ def test_rotation_sees_relative_positions_only(sv):
     b, _ = rc.recombine_fwd(Q, K, V, pq + 1_000_000, pk + 1_000_000, groups, rot)
     torch.cuda.synchronize()
     assert rel(a, b.double()) <= REL
+
+
+def test_padded_batch(sv):
+    """Rows behind the last group: zero gradients there, and the weights' gradients are those of the rows before."""
+    from sparse_convolution_pruned_b200 import recombine as rc
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    Q, K, V, dO = rnd(90, 4, 64).bfloat16(), rnd(400, 2, 64).bfloat16(), rnd(400, 2, 64).bfloat16(), rnd(90, 4, 64).bfloat16()
+    wq, wk = 1 + 0.2 * rnd(64), 1 + 0.2 * rnd(64)
+    pq, pk = torch.arange(90, dtype=torch.int32, device="cuda"), torch.arange(400, dtype=torch.int32, device="cuda")
+    off = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    groups, rot = rc.Groups(off(0, 20, 70), off(0, 110, 310), 50, 200), rc.Rotation(rc.axis_frequencies((32,)), (32,))
+
+    def grads(nq, nk):
+        _, saved = rc.recombine_fwd(Q[:nq], K[:nk], V[:nk], pq[:nq], pk[:nk], groups, rot, wq=wq, wk=wk)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]  # what memory may hold
+        del junk
+        return rc.recombine_bwd(dO[:nq], saved, groups, rot)
+
+    exact, padded = grads(70, 310), grads(90, 400)
+    torch.cuda.synchronize()
+    for a, b in zip(exact[:3], padded[:3]):
+        assert torch.equal(a, b[:len(a)]) and (b[len(a):] == 0).all()
+    for a, b in zip(exact[3:], padded[3:]):  # the same terms and zeros, summed in another order
+        assert rel(b, a.double()) <= REL
+
+
+def test_scratch_of_a_call_on_another_stream(sv, monkeypatch):
+    """Scratch memory that a call allocates is not given out again while its stream has the call before it."""
+    taken = []
+    scratch = sv._scratch
+
+    def spy(*args):
+        got = scratch(*args)
+        taken.append(got[1:])
+        return got
+    monkeypatch.setattr(sv, "_scratch", spy)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    off = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    Q, K, V = rnd(3, 2, 64).bfloat16(), rnd(9000, 2, 64).bfloat16(), rnd(9000, 2, 64).bfloat16()
+    lim, g = dict(max_q=3, max_kv=9000), rnd(5000)
+    pos, freq = (torch.arange(n, dtype=torch.int32, device="cuda") for n in (3, 9000)), torch.ones(32, dtype=torch.float64, device="cuda")
+    pq, pk = pos
+    calls = [
+        lambda s: sv.svconv_cross_attn_fwd(Q, K, V, off3, off9, stream=s, **lim),
+        lambda s: sv.svconv_cross_attn_bwd(Q, Q, K, V, O, lse, off3, off9, stream=s, **lim),
+        lambda s: sv.svconv_qk_norm_rope_bwd(Q, K, Q, K, pq, pk, freq, stream=s),
+        lambda s: sv.svconv_clip_grads([g], 1.0, stream=s),
+    ]
+    off3, off9 = off(3), off(9000)
+    O, lse = sv.svconv_cross_attn_fwd(Q, K, V, off3, off9, **lim)
+    side = torch.cuda.Stream()
+    for call in calls:
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        del taken[:]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # ~0.1 s
+        call(side)
+        (address, size), = taken
+        assert size > 0
+        fresh = [torch.empty((size,), dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(t.data_ptr() != address for t in fresh)
+    torch.cuda.synchronize()
+    assert sv.svconv_read_error_word() == 0
