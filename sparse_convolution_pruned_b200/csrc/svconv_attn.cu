@@ -1266,6 +1266,307 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
   if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------- backward, few queries
+// Groups whose queries fit one tile of 32 packed rows (CLS and auxiliary tokens): that tile stays in shared memory and
+// the keys stream past it once.  Every key has its gradients from this tile alone, so they are written as they
+// come, and dQ is the only sum: K is read once and each score is computed once (5 products a tile).
+//     S^T = K Q^T, dP^T = V dO^T;  dV = P^T dO, dK = dS^T Q (P^T, dS^T in tensor memory);  dQ^T += K^T dS
+// For the last one dS^T goes to shared memory too, one row per key, which makes it an MN-major B operand, and K's
+// tile is read as an MN-major A.  Two streams take alternate key tiles; at 128 channels they share the accumulators.
+constexpr int kFew = 32;
+constexpr int kFewBlock = kFew * 128;  // bytes of the tile's 64-channel block
+
+struct FewBarriers {
+  uint64_t qfull, qready, kvfull[10], kvempty[10], kready[10], sfull[2], sread[2], pfull[2], adone[2], qdone[2], oread, fin[2];
+  uint32_t kept[10][4];  // keys of the slot's tile that take part
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int DB>
+struct FewShape {
+  static constexpr int kTileBytes = DB * kBlockBytes;
+  static constexpr int kStages = DB == 1 ? 10 : 4;  // K and V tiles in turn
+  static constexpr int kdS = 2 * DB * kFewBlock, kRing = kdS + 2 * kBlockBytes, kStatAt = kRing + kStages * kTileBytes;
+  static constexpr size_t kSmem = 1024 + kStatAt + kStatBytes + sizeof(FewBarriers);
+  static constexpr int kStride = DB == 1 ? 224 : 96;
+  static constexpr int S(int s) { return s * kStride; }
+  static constexpr int dP(int s) { return s * kStride + 32; }
+  static constexpr int P(int s) { return s * kStride + 64; }
+  static constexpr int dS(int s) { return s * kStride + 80; }
+  static constexpr int dV(int s) { return DB == 1 ? s * kStride + 96 : 192; }
+  static constexpr int dK(int s) { return DB == 1 ? s * kStride + 160 : 320; }
+  static constexpr int kQ = 448;  // dQ^T: a channel a lane, a packed row a column
+};
+
+template <int DB>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_constant__ BwdParams p) {
+  using Sh = FewShape<DB>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
+  const float* stat = reinterpret_cast<const float*>(aligned + Sh::kStatAt);
+  FewBarriers* bar = reinterpret_cast<FewBarriers*>(aligned + Sh::kStatAt + kStatBytes);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bar->abort_flag;
+  int* err = p.status;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar->qfull, 1), mbar_init(&bar->qready, 1), mbar_init(&bar->oread, 8);
+    // K's slots are the even ones: their readers are the products and the check warp
+    for (int i = 0; i < NS; ++i) mbar_init(&bar->kvfull[i], 1), mbar_init(&bar->kvempty[i], 2 - (i & 1)), mbar_init(&bar->kready[i], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->sfull[s], 1), mbar_init(&bar->sread[s], 8), mbar_init(&bar->pfull[s], 8);
+      mbar_init(&bar->adone[s], 1), mbar_init(&bar->qdone[s], 1), mbar_init(&bar->fin[s], 1);
+    }
+    bar->abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&p.mq), prefetch_tmap(&p.mdo), prefetch_tmap(&p.fk), prefetch_tmap(&p.fv);
+  }
+  if (warp == kSumWarp) {
+    tmem_alloc(&bar->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  int item = blockIdx.x;
+  const int hk = item % p.Hkv;
+  item /= p.Hkv;
+  const int split = item % p.qsplits, g = item / p.qsplits;
+  int q0, q1, k0, k1;
+  const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
+  if (flags && threadIdx.x == 0 && split == 0 && hk == 0) atomicOr(p.status, flags);
+  const bool bad = flags & SVCONV_STATUS_BAD_OFFSETS;
+  const int rows = bad ? 0 : (q1 - q0) * p.r, tiles = bad ? 0 : (k1 - k0 + kTile - 1) / kTile;
+  const int t_lo = (int)((int64_t)tiles * split / p.qsplits), t_hi = (int)((int64_t)tiles * (split + 1) / p.qsplits);
+  const int nt = rows > 0 ? t_hi - t_lo : 0, key0 = k0 + t_lo * kTile;
+  auto partial = [&](int t) { return p.keep || key0 + (t + 1) * kTile > k1; };
+
+  int loaded = 0;
+  if (warp == kLoadWarp) {
+    if (lane == 0 && nt > 0) {
+      const int tokens = kFew / p.r;
+      mbar_arrive_expect_tx(&bar->qfull, (uint32_t)(tokens * p.r) * 256u * DB + (uint32_t)kStatBytes);
+      for (int b = 0; b < DB; ++b) {
+        tma_load_4d(base + b * kFewBlock, &p.mq, &bar->qfull, b * 64, 0, hk, q0);
+        tma_load_4d(base + (DB + b) * kFewBlock, &p.mdo, &bar->qfull, b * 64, 0, hk, q0);
+      }
+      bulk_copy_g2s(base + Sh::kStatAt, p.stat + ((int64_t)hk * p.stat_tiles + q0 / (kMove / p.r) + g) * kStat, kStatBytes, &bar->qfull);
+      for (; loaded < 2 * nt; ++loaded) {
+        const int slot = loaded % NS;
+        if (loaded >= NS) wait_for(&bar->kvempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+        if (*abort_flag) break;
+        mbar_arrive_expect_tx(&bar->kvfull[slot], Sh::kTileBytes);
+        for (int b = 0; b < DB; ++b)
+          tma_load_3d(base + Sh::kRing + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.fv : &p.fk, &bar->kvfull[slot], b * 64,
+                      hk, key0 + (loaded >> 1) * kTile);
+      }
+    }
+  } else if (warp == kScoreWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const int ks = (p.d + 15) / 16, n = uniform(nt);
+      const uint32_t idesc = idesc_bf16_f32(kTile, kFew, 0, 0), tm = uniform(tmem);
+      const uint64_t dq = smem_desc_sw128(base, 16, 1024), dkv = smem_desc_sw128(base + Sh::kRing, 16, 1024);
+      // operand o (0: K Q, 1: V dO)
+      auto scores = [&](int o, int slot, uint32_t d) {
+        const uint64_t a0 = dkv + (uint64_t)(slot * (Sh::kTileBytes >> 4)), b0 = dq + (uint64_t)(o * DB * (kFewBlock >> 4));
+#pragma unroll
+        for (int k = 0; k < 4 * DB; ++k)
+          if (k < ks)
+            mma_ss(d, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), b0 + (uint64_t)((k >> 2) * (kFewBlock >> 4) + (k & 3) * 2),
+                   idesc, k ? 1u : 0u, e);
+      };
+      wait_warp(&bar->qready, 0, abort_flag, err);
+      for (int t = 0; t < n; ++t) {
+        const int s = t & 1, i = t >> 1, k = 2 * t, v = k + 1;
+        wait_warp(&bar->kvfull[k % NS], (k / NS) & 1, abort_flag, err);
+        if (i > 0) wait_warp(&bar->sread[s], (i - 1) & 1, abort_flag, err);  // the columns are free
+        tc_fence_after();
+        scores(0, k % NS, tm + Sh::S(s));
+        wait_warp(&bar->kvfull[v % NS], (v / NS) & 1, abort_flag, err);
+        tc_fence_after();
+        scores(1, v % NS, tm + Sh::dP(s));
+        commit_to(&bar->sfull[s], e);
+        commit_to(&bar->kvempty[v % NS], e);
+      }
+      commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
+      wait_warp(&bar->fin[0], 0, abort_flag, err);
+    }
+  } else if (warp == kSumWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const int n = uniform(nt);
+      const uint32_t tm = uniform(tmem), idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), idesc_q = idesc_bf16_f32(kTile, kFew, 1, 1);
+      const uint64_t dq = smem_desc_sw128(base, kFewBlock, 1024), dgo = smem_desc_sw128(base + DB * kFewBlock, kFewBlock, 1024);
+      // up to 64 channels A's second half of rows is the next slot's V tile: rows of dQ^T that are not read
+      const uint64_t dk = smem_desc_sw128(base + Sh::kRing, kBlockBytes, 1024), dds = smem_desc_sw128(base + Sh::kdS, kBlockBytes, 1024);
+      for (int t = 0; t < n; ++t) {
+        const int s = t & 1, i = t >> 1, slot = 2 * t % NS;
+        wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
+        if (DB == 2 && t > 0) wait_warp(&bar->oread, (t - 1) & 1, abort_flag, err);  // the accumulators are free
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kFew / 16; ++k) {
+          mma_ts(tm + Sh::dV(s), tm + Sh::P(s) + k * 8, dgo + (uint64_t)(k * (2048 >> 4)), idesc, k ? 1u : 0u, e);
+          mma_ts(tm + Sh::dK(s), tm + Sh::dS(s) + k * 8, dq + (uint64_t)(k * (2048 >> 4)), idesc, k ? 1u : 0u, e);
+        }
+        commit_to(&bar->adone[s], e);
+        if (partial(t)) wait_warp(&bar->kready[slot], (2 * t / NS) & 1, abort_flag, err);  // keys that take no part are zero
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ss(tm + Sh::kQ, dk + (uint64_t)(slot * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dds + (uint64_t)(s * (kBlockBytes >> 4) + k * (2048 >> 4)),
+                 idesc_q, t || k ? 1u : 0u, e);
+        commit_to(&bar->qdone[s], e);
+        commit_to(&bar->kvempty[slot], e);
+      }
+      commit_to(&bar->fin[1], e);
+      wait_warp(&bar->fin[1], 0, abort_flag, err);
+    }
+  } else if (warp == kCheckWarp) {
+    if (nt > 0) {
+      wait_warp(&bar->qfull, 0, abort_flag, err);
+      if (rows < kFew) {
+        const uint32_t w[1] = {~0u << rows};
+        scrub_rows(base, 2 * DB, kFewBlock, w);
+      }
+      warp_arrive(&bar->qready);
+    }
+    for (int t = 0; t < nt; ++t) {
+      const int slot = 2 * t % NS;
+      wait_warp(&bar->kvfull[slot], (2 * t / NS) & 1, abort_flag, err);
+      if (partial(t)) {
+        uint32_t w[4];
+        kept_words(p.keep, key0 + t * kTile, k1, w);
+        if (lane < 4) bar->kept[slot][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ~w[i];
+        scrub_rows(base + Sh::kRing + slot * Sh::kTileBytes, DB, kBlockBytes, w);
+      }
+      warp_arrive(&bar->kready[slot]);
+      warp_arrive(&bar->kvempty[slot]);
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS and the outputs: two threads per key
+    const int s = warp >> 3, h = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const f2 c2 = pack2(p.c, p.c);
+    if (nt > 0) wait_warp(&bar->qfull, 0, abort_flag, err);
+    for (int t = s; t < nt; t += 2) {
+      const int i = t >> 1, slot = 2 * t % NS;
+      wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
+      tc_fence_after();
+      uint32_t a[16], b[16], w[8], u[8];
+      tmem_ld_x16(tmem + lanes + Sh::S(s) + h * 16, a);
+      tmem_ld_x16(tmem + lanes + Sh::dP(s) + h * 16, b);
+      tmem_ld_wait();
+      tc_fence_before();
+      warp_arrive(&bar->sread[s]);
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) {  // a row that does not exist has -lse = -inf: weight 0
+        const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(stat + h * 16 + k);
+        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(stat + kMove + h * 16 + k);
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          float x, y;
+          unpack2(fma2(pack2(a[k + j], a[k + j + 1]), c2, j ? nl.y : nl.x), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          w[(k + j) / 2] = pack_bf16(x, y);
+          unpack2(mul2(pack2(x, y), add2(pack2(b[k + j], b[k + j + 1]), j ? nd.y : nd.x)), x, y);
+          u[(k + j) / 2] = pack_bf16(x, y);
+        }
+      }
+      if (partial(t)) {
+        wait_warp(&bar->kready[slot], (2 * t / NS) & 1, abort_flag, err);
+        if (!(bar->kept[slot][warp & 3] >> lane & 1u)) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = u[k] = 0u;
+        }
+      }
+      tmem_st_x8(tmem + lanes + Sh::P(s) + h * 8, w);
+      tmem_st_x8(tmem + lanes + Sh::dS(s) + h * 8, u);
+      if (i > 0) wait_warp(&bar->qdone[s], (i - 1) & 1, abort_flag, err);  // dS in shared memory is free again
+      const uint32_t ds = base + Sh::kdS + s * kBlockBytes + row * 128;
+      st_shared_16(ds + ((h * 2) ^ (row & 7)) * 16, u[0], u[1], u[2], u[3]);
+      st_shared_16(ds + ((h * 2 + 1) ^ (row & 7)) * 16, u[4], u[5], u[6], u[7]);
+      fence_proxy_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&bar->pfull[s]);
+      wait_warp(&bar->adone[s], i & 1, abort_flag, err);
+      tc_fence_after();
+      // half 0 writes dV, half 1 dK
+      const int key = key0 + t * kTile + row;
+      const float f = h ? p.scale : 1.f;
+      __nv_bfloat16* out = (h ? p.dK : p.dV) + ((int64_t)key * p.Hkv + hk) * p.d;
+      const int acc = h ? Sh::dK(s) : Sh::dV(s);
+#pragma unroll 1
+      for (int c = 0; c < p.d; c += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tmem + lanes + acc + c, o);
+        tmem_ld_wait();
+        if (key < k1) {
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) * f;
+          store_row(out + c, v, p.d - c, p.wide);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[16 + k]) * f;
+          store_row(out + c + 16, v, p.d - c - 16, p.wide);
+        }
+      }
+      if (DB == 2) {
+        tc_fence_before();
+        warp_arrive(&bar->oread);
+      }
+    }
+    if (nt > 0) wait_warp(&bar->fin[1], 0, abort_flag, err);
+    tc_fence_after();
+    // dQ: 8 packed rows a warpgroup, a channel a thread
+    if (rows > 0) {
+      const int part = warp >> 2;
+      uint32_t o[8];
+      if (nt > 0) {
+        tmem_ld_x8(tmem + lanes + Sh::kQ + part * 8, o);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int q = part * 8 + k;
+        if (q >= rows || row >= p.d) continue;
+        const int64_t at = ((int64_t)(q0 + q / p.r) * p.Hq + hk * p.r + q % p.r) * p.d + row;
+        const float v = nt > 0 ? __uint_as_float(o[k]) * p.scale : 0.f;
+        if (p.qsplits > 1) p.part_q[split * ((int64_t)p.nq * p.Hq * p.d) + at] = v;
+        else p.dQ[at] = __float2bfloat16(v);
+      }
+    } else if (!bad) {  // keys without queries
+      const int chunks = p.d / 8;
+      for (int i = threadIdx.x; i < (min(k1, k0 + t_hi * kTile) - key0) * chunks; i += kSoftWarps * 32) {
+        const int64_t at = ((int64_t)(key0 + i / chunks) * p.Hkv + hk) * p.d + i % chunks * 8;
+        *reinterpret_cast<uint4*>(p.dK + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(p.dV + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (bar->abort_flag && warp == kLoadWarp && lane == 0 && nt > 0) {
+    // a wait ran out somewhere: let the copies in flight land before the CTA gives its memory back
+    volatile int never = 0;
+    mbar_wait(&bar->qfull, 0, &never, err, kDefaultTimeoutNs);
+    for (int i = loaded > NS ? loaded - NS : 0; i < loaded; ++i)
+      mbar_wait(&bar->kvfull[i % NS], (i / NS) & 1, &never, err, kDefaultTimeoutNs);
+  }
+  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
+}
+
 // -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
 // key pass reads them: group g's tiles start at tile q_off[g] / tokens + g, which leaves room for each
 // group's last, partly filled one.  Rows that do not exist, and rows without any key, get -inf and 0, so
@@ -1444,8 +1745,10 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
 // half an SM's share of all work, by that schedule's end plus the cost of the partial results.  In units of one
 // moving tile of the query pass (about 0.6 us).
 constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kBwdMerge = 5.0, kBwdMergeBytes = 3.0e6;
+constexpr double kFewTile = 1.5, kFewFixed = 8.0, kFewMerge = 5.0;
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits, keys_first;
+  int few;              // the kernel for few queries, with qsplits cuts of the keys
   int tiles;            // of statistics, for each key head
   size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
   size_t floats() const { return stat + pq + 2 * pk; }
@@ -1504,6 +1807,17 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
                        (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? 2 * kBwdMerge + bk * sk : 0.0);
       if (best == 0.0 || t < best) best = t, b.qsplits = sq, b.ksplits = sk, b.keys_first = kf;
     }
+  b.few = c.max_q > 0 && c.max_kv > 0 && (int64_t)c.max_q * r <= kFew;
+  if (b.few) {  // one item a split of a group's keys and key head
+    const int tiles = cdiv(c.max_kv, kTile);
+    const double units = (double)G * c.Hkv, tile = c.d <= 64 ? kFewTile : 2 * kFewTile;
+    best = 0.0;
+    b.ksplits = 1;
+    for (int s = 1; s <= tiles && (s == 1 || units * s <= 8.0 * kSms); ++s) {
+      const double t = std::ceil(units * s / kSms) * (cdiv(tiles, s) * tile + kFewFixed) + (s > 1 ? kFewMerge + bq * s : 0.0);
+      if (best == 0.0 || t < best) best = t, b.qsplits = s;
+    }
+  }
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
   b.tiles = c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
@@ -1517,6 +1831,13 @@ cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t s) {
   static int done[64];
   cudaError_t e = ensure_smem_attr(attn_bwd_kernel<DB>, BwdShape<DB>::kSmem, done);
   return e == cudaSuccess ? launch_pdl(attn_bwd_kernel<DB>, dim3(grid), dim3(kThreads), BwdShape<DB>::kSmem, s, p) : e;
+}
+
+template <int DB>
+cudaError_t launch_few(const BwdParams& p, int grid, cudaStream_t s) {
+  static int done[64];
+  cudaError_t e = ensure_smem_attr(attn_bwd_few_kernel<DB>, FewShape<DB>::kSmem, done);
+  return e == cudaSuccess ? launch_pdl(attn_bwd_few_kernel<DB>, dim3(grid), dim3(kThreads), FewShape<DB>::kSmem, s, p) : e;
 }
 
 template <int DB>
@@ -1609,7 +1930,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   if ((rc = check_device())) return rc;
   const BwdPlan b = plan_bwd(c);
   const long long heads = (long long)c.G * c.Hkv;
-  const long long q_items = heads * b.qblocks * b.qsplits, k_items = heads * b.kblocks * b.ksplits;
+  const long long q_items = heads * (b.few ? 1 : b.qblocks) * b.qsplits, k_items = b.few ? 0 : heads * b.kblocks * b.ksplits;
   const int r = c.Hq / c.Hkv;
   int lanes = 1;
   while (lanes < c.d / 8) lanes *= 2;
@@ -1639,9 +1960,9 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   const void *q = c.nq ? Q : K, *go = c.nq ? dO : K, *k = c.nkv ? K : Q, *v = c.nkv ? V : Q;
   const int64_t go_row = (int64_t)c.Hq * c.d, go_head = c.d;
   if (!make_packed_map(&p.fq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, kTile / r) ||
-      !make_packed_map(&p.mq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, kMove / r) ||
+      !make_packed_map(&p.mq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, (b.few ? kFew : kMove) / r) ||
       !make_packed_map(&p.fdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, kTile / r) ||
-      !make_packed_map(&p.mdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, kMove / r) ||
+      !make_packed_map(&p.mdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, (b.few ? kFew : kMove) / r) ||
       !make_rows_map(&p.fk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kTile) ||
       !make_rows_map(&p.mk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kMove) ||
       !make_rows_map(&p.fv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kTile) ||
@@ -1652,7 +1973,9 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   if (c.max_q > 0)
     e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid, c.G), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
                    static_cast<const __nv_bfloat16*>(O), lse, c.q_off, c.nq, c.max_q, c.Hq, c.Hkv, c.d, lanes, b.tiles, ws);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && b.few)
+    e = c.d <= 64 ? launch_few<1>(p, (int)q_items, s) : launch_few<2>(p, (int)q_items, s);
+  else if (e == cudaSuccess)
     e = c.d <= 64 ? launch_bwd<1>(p, (int)(q_items + k_items), s) : launch_bwd<2>(p, (int)(q_items + k_items), s);
   auto add = [&](const float* part, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound, int H,
                  __nv_bfloat16* out) {

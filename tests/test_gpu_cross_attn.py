@@ -205,6 +205,48 @@ def test_rows_beyond_32_bit_offsets(sv):
     assert not dK[300:n - 600].any() and not dV[300:n - 600].any()
 
 
+FEW = [  # at most 32 query rows (tokens x heads of a key head) a group
+    ((16, 16, 16, 16), (900, 1300, 1, 640), 4, 4, 64, 1.0, 0, False),
+    ((32,), (5000,), 1, 1, 128, 1.0, 0, False),
+    ((31, 0, 7), (300, 200, 0), 2, 2, 64, 0.7, 2, True),
+    ((10, 3), (1000, 129), 3, 1, 96, 0.9, 1, False),
+    ((1, 0, 1), (4000, 500, 127), 32, 1, 128, 0.5, 3, False),
+    ((4, 2), (257, 3000), 24, 4, 40, 1.0, 0, True),
+    ((5, 5, 5), (128, 128, 256), 5, 5, 8, 0.2, 0, False),
+    ((2,) * 40, tuple(range(0, 400, 10)), 8, 2, 80, 0.9, 0, False),
+    ((8, 1), (20000, 31), 4, 1, 64, 1.0, 0, False),
+]
+
+
+@pytest.mark.parametrize("i", range(len(FEW)))
+def test_few_queries(sv, i):
+    q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused = FEW[i]
+    x = make(60 + i, q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused)
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, f"few queries {i}")
+    again = run_both(sv, x)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_queries_among_rows_that_hold_anything(sv, d):
+    """NaN and infinities in dropped keys and in rows of other groups and of no group, behind short query tiles."""
+    x = make(77, (5, 9), (300, 700), 2, 2, d, keep=0.6, gap=9)
+    want = run_both(sv, x)
+    qo, ko = x["q_off"].tolist(), x["kv_off"].tolist()
+    out_q = torch.ones(x["Q"].shape[0], dtype=torch.bool, device="cuda")
+    out_q[qo[0]:qo[-1]] = False
+    drop = x["keep"] == 0
+    drop[:ko[0]], drop[ko[-1]:] = True, True
+    for n, k in enumerate(("K", "V")):
+        x[k][drop] = float("nan") if n else float("inf")
+    for k in ("Q", "dO"):
+        x[k][out_q] = float("nan")
+    got = run_both(sv, x)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+
+
 def test_many_groups(sv):
     """More groups than a warp has lanes, lengths from 0 on, some groups empty on either side."""
     rng = np.random.default_rng(5)
