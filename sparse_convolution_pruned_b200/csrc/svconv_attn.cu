@@ -921,6 +921,8 @@ struct BwdParams {
   int wide;                      // rows of the gradients start on 32-byte boundaries
   const float* stat;             // [Hkv][stat_tiles][kStat], see attn_stat_kernel
   int stat_tiles;
+  const __nv_bfloat16 *dO, *O;   // few queries: the kernel takes the statistics itself
+  const float* lse;
   __nv_bfloat16 *dQ, *dK, *dV;
   float *part_q, *part_k, *part_v;  // [splits][rows][d] where a pass is split
   int* status;
@@ -1272,7 +1274,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 // come, and dQ is the only sum: K is read once and each score is computed once (5 products a tile).
 //     S^T = K Q^T, dP^T = V dO^T;  dV = P^T dO, dK = dS^T Q (P^T, dS^T in tensor memory);  dQ^T += K^T dS
 // For the last one dS^T goes to shared memory too, one row per key, which makes it an MN-major B operand, and K's
-// tile is read as an MN-major A.  Two streams take alternate key tiles; at 128 channels they share the accumulators.
+// tile is read as an MN-major A.  The tile's statistics (-lse in base 2 and -D of its rows) are taken in the kernel: a
+// launch before it costs more.  Two streams take alternate key tiles; at 128 channels they share the accumulators.
 constexpr int kFew = 32;
 constexpr int kFewBlock = kFew * 128;  // bytes of the tile's 64-channel block
 
@@ -1288,7 +1291,7 @@ struct FewShape {
   static constexpr int kTileBytes = DB * kBlockBytes;
   static constexpr int kStages = DB == 1 ? 10 : 4;  // K and V tiles in turn
   static constexpr int kdS = 2 * DB * kFewBlock, kRing = kdS + 2 * kBlockBytes, kStatAt = kRing + kStages * kTileBytes;
-  static constexpr size_t kSmem = 1024 + kStatAt + kStatBytes + sizeof(FewBarriers);
+  static constexpr size_t kSmem = 1024 + kStatAt + 2 * kFew * sizeof(float) + sizeof(FewBarriers);
   static constexpr int kStride = DB == 1 ? 224 : 96;
   static constexpr int S(int s) { return s * kStride; }
   static constexpr int dP(int s) { return s * kStride + 32; }
@@ -1306,8 +1309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
-  const float* stat = reinterpret_cast<const float*>(aligned + Sh::kStatAt);
-  FewBarriers* bar = reinterpret_cast<FewBarriers*>(aligned + Sh::kStatAt + kStatBytes);
+  float* stat = reinterpret_cast<float*>(aligned + Sh::kStatAt);
+  FewBarriers* bar = reinterpret_cast<FewBarriers*>(aligned + Sh::kStatAt + 2 * kFew * sizeof(float));
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* abort_flag = &bar->abort_flag;
   int* err = p.status;
@@ -1351,12 +1354,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
   if (warp == kLoadWarp) {
     if (lane == 0 && nt > 0) {
       const int tokens = kFew / p.r;
-      mbar_arrive_expect_tx(&bar->qfull, (uint32_t)(tokens * p.r) * 256u * DB + (uint32_t)kStatBytes);
+      mbar_arrive_expect_tx(&bar->qfull, (uint32_t)(tokens * p.r) * 256u * DB);
       for (int b = 0; b < DB; ++b) {
         tma_load_4d(base + b * kFewBlock, &p.mq, &bar->qfull, b * 64, 0, hk, q0);
         tma_load_4d(base + (DB + b) * kFewBlock, &p.mdo, &bar->qfull, b * 64, 0, hk, q0);
       }
-      bulk_copy_g2s(base + Sh::kStatAt, p.stat + ((int64_t)hk * p.stat_tiles + q0 / (kMove / p.r) + g) * kStat, kStatBytes, &bar->qfull);
       for (; loaded < 2 * nt; ++loaded) {
         const int slot = loaded % NS;
         if (loaded >= NS) wait_for(&bar->kvempty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
@@ -1457,7 +1459,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
     const int s = warp >> 3, h = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const f2 c2 = pack2(p.c, p.c);
-    if (nt > 0) wait_warp(&bar->qfull, 0, abort_flag, err);
+    if (nt > 0) {
+      // -lse in base 2 and -D: a warp a row; rows that do not exist or have no key get weight 0
+#pragma unroll
+      for (int q = warp; q < kFew; q += kSoftWarps) {
+        const int64_t at = (int64_t)(q0 + q / p.r) * p.Hq + hk * p.r + q % p.r;
+        float v = 0.f;
+        if (q < rows && lane * 4 < p.d) {
+          const uint2 x = *reinterpret_cast<const uint2*>(p.dO + at * p.d + lane * 4), y = *reinterpret_cast<const uint2*>(p.O + at * p.d + lane * 4);
+          v = __uint_as_float(x.x << 16) * __uint_as_float(y.x << 16);
+          v = fmaf(__uint_as_float(x.x & 0xffff0000u), __uint_as_float(y.x & 0xffff0000u), v);
+          v = fmaf(__uint_as_float(x.y << 16), __uint_as_float(y.y << 16), v);
+          v = fmaf(__uint_as_float(x.y & 0xffff0000u), __uint_as_float(y.y & 0xffff0000u), v);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) {
+          const float l = q < rows ? p.lse[at] : -INFINITY;
+          stat[q] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+          stat[kFew + q] = -v;
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory");
+    }
     for (int t = s; t < nt; t += 2) {
       const int i = t >> 1, slot = 2 * t % NS;
       wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
@@ -1471,7 +1495,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < 16; k += 4) {  // a row that does not exist has -lse = -inf: weight 0
         const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(stat + h * 16 + k);
-        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(stat + kMove + h * 16 + k);
+        const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(stat + kFew + h * 16 + k);
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           float x, y;
@@ -1606,23 +1630,42 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const __nv_bfloat16* __r
   }
 }
 
-// The splits of a gradient added in order: 8 channels a thread over the rows of group blockIdx.y.
+// The splits of a gradient added up: 8 channels a thread over the rows of group blockIdx.y, by SLICES warps of the block
+// that take every SLICES-th split and whose sums are added in order.  One slice moves the most bytes; eight
+// shorten the chain of loads where there are many splits (148 of 32 rows: a call of 22.7 us takes 14.5).
+template <int SLICES>
 __global__ void __launch_bounds__(256) attn_sum_kernel(const float* __restrict__ part, int splits, const int32_t* off, const int32_t* off2,
                                                        int n, int n2, int bound, int H, int d, __nv_bfloat16* __restrict__ out) {
+  constexpr int kThreadsX = 256 / SLICES;
+  __shared__ float s_v[SLICES > 1 ? SLICES : 1][SLICES > 1 ? kThreadsX : 1][9];
+  const int x = threadIdx.x % kThreadsX, y = threadIdx.x / kThreadsX;
   pdl_wait();
   pdl_trigger();
   int lo, hi, lo2, hi2;
   const int flags = group_range(off, blockIdx.y, n, bound, lo, hi) | group_range(off2, blockIdx.y, n2, n2, lo2, hi2);
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if ((flags & SVCONV_STATUS_BAD_OFFSETS) || i >= (int64_t)(hi - lo) * H * d) return;
+  const int64_t i = ((int64_t)blockIdx.x * kThreadsX + x) * 8;
+  const bool on = !(flags & SVCONV_STATUS_BAD_OFFSETS) && i < (int64_t)(hi - lo) * H * d;
   const int64_t at = (int64_t)lo * H * d + i, step = (int64_t)n * H * d;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (on) {
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 a = *reinterpret_cast<const float4*>(part + s * step + at), b = *reinterpret_cast<const float4*>(part + s * step + at + 4);
-    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    for (int s = y; s < splits; s += SLICES) {
+      const float4 a = *reinterpret_cast<const float4*>(part + s * step + at), b = *reinterpret_cast<const float4*>(part + s * step + at + 4);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
   }
-  *reinterpret_cast<uint4*>(out + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  if constexpr (SLICES > 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_v[y][x][k] = v[k];
+    __syncthreads();
+    if (y > 0) return;
+#pragma unroll
+    for (int w = 1; w < SLICES; ++w)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += s_v[w][x][k];
+  }
+  if (on)
+    *reinterpret_cast<uint4*>(out + at) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 // ---------------------------------------------------------------------------- host side
@@ -1745,6 +1788,7 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
 // half an SM's share of all work, by that schedule's end plus the cost of the partial results.  In units of one
 // moving tile of the query pass (about 0.6 us).
 constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kBwdMerge = 5.0, kBwdMergeBytes = 3.0e6;
+// Few queries: microseconds of a key tile of 64 channels, of a CTA beside its tiles, and of adding the splits up.
 constexpr double kFewTile = 1.5, kFewFixed = 8.0, kFewMerge = 5.0;
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits, keys_first;
@@ -1819,7 +1863,7 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
     }
   }
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
-  b.tiles = c.nq / (kMove / r) + c.G + 1;
+  b.tiles = b.few ? 0 : c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
   b.pq = b.qsplits > 1 ? b.qsplits * nq * c.d : 0;
   b.pk = b.ksplits > 1 ? b.ksplits * nk * c.d : 0;
@@ -1948,6 +1992,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   p.scale = c.scale;
   p.stat = ws;
   p.stat_tiles = b.tiles;
+  p.dO = static_cast<const __nv_bfloat16*>(dO), p.O = static_cast<const __nv_bfloat16*>(O), p.lse = lse;
   p.part_q = ws + b.stat;
   p.part_k = p.part_q + b.pq;
   p.part_v = p.part_k + b.pk;
@@ -1970,7 +2015,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (c.max_q > 0)
+  if (c.max_q > 0 && !b.few)
     e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid, c.G), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
                    static_cast<const __nv_bfloat16*>(O), lse, c.q_off, c.nq, c.max_q, c.Hq, c.Hkv, c.d, lanes, b.tiles, ws);
   if (e == cudaSuccess && b.few)
@@ -1980,8 +2025,9 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   auto add = [&](const float* part, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound, int H,
                  __nv_bfloat16* out) {
     if (e != cudaSuccess || splits < 2) return;
-    const long long grid = ((long long)bound * H * c.d / 8 + 255) / 256;
-    e = launch_pdl(attn_sum_kernel, dim3((unsigned)grid, c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out);
+    const long long chunks = (long long)bound * H * c.d / 8;
+    e = splits > 8 ? launch_pdl(attn_sum_kernel<8>, dim3((unsigned)((chunks + 31) / 32), c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out)
+                   : launch_pdl(attn_sum_kernel<1>, dim3((unsigned)((chunks + 255) / 256), c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out);
   };
   add(p.part_q, b.qsplits, c.q_off, c.kv_off, c.nq, c.nkv, c.max_q, c.Hq, p.dQ);
   add(p.part_k, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dK);
