@@ -1271,7 +1271,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 // ---------------------------------------------------------------------------- backward, few queries
 // Groups whose queries fit one tile of 32 packed rows (CLS and auxiliary tokens): that tile stays in shared memory and
 // the keys stream past it once.  Every key has its gradients from this tile alone, so they are written as they
-// come, and dQ is the only sum: K is read once and each score is computed once (5 products a tile).
+// come, and dQ is the only sum: K is read once and each score is computed once (5 products a tile; 4 x 16 queries over
+// 9,000 keys, 4 heads of 64: 22.6 us against 53.4 by the two passes).
 //     S^T = K Q^T, dP^T = V dO^T;  dV = P^T dO, dK = dS^T Q (P^T, dS^T in tensor memory);  dQ^T += K^T dS
 // For the last one dS^T goes to shared memory too, one row per key, which makes it an MN-major B operand, and K's
 // tile is read as an MN-major A.  The tile's statistics (-lse in base 2 and -D of its rows) are taken in the kernel: a
@@ -1591,6 +1592,309 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
   if (warp == kSumWarp) tmem_dealloc(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------- backward, few keys
+// Groups of at most 96 keys (an encoder's states, a handful of landmarks) under many queries: the keys stay in shared
+// memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 52 us
+// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 116 against 147).
+//     S = Q K^T, dP = dO V^T;  dQ = dS K, written as it comes;  dV^T += dO^T P, dK^T += Q^T dS
+// P and dS go to shared memory, a row per query: K-major as the A operand of dQ, MN-major as the B operands of the sums,
+// whose A operands are the query tiles read MN-major.  Four threads share a query row, so that few registers hold a tile;
+// two groups of warps on alternate tiles gained 4% at 64 channels and lost 15% at 128, where P and dS have one place.
+constexpr int kFewKeys = 96;
+constexpr int kFewKeyBlock = kFewKeys * 128;  // bytes of a 64-channel block of the keys
+
+struct FewKeyBarriers {
+  uint64_t kfull, kready, full[8], empty[8], ready[8], sfull, sread, pfull, qdone, sdone, fin[2];
+  uint32_t kept[4];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int DB>
+struct FewKeyShape {
+  static constexpr int kTileBytes = DB * kBlockBytes;
+  static constexpr int kStages = DB == 1 ? 8 : 3;  // Q and dO tiles in turn
+  static constexpr int kRing = 2 * DB * kFewKeyBlock, kP = kRing + kStages * kTileBytes, kdS = kP + 2 * kBlockBytes, kBar = kdS + 2 * kBlockBytes;
+  static constexpr size_t kSmem = 1024 + kBar + sizeof(FewKeyBarriers);
+  // tensor memory: the scores, dQ, and dV^T, dK^T with a channel a lane and a key a column
+  static constexpr int kTmS = 0, kTmdP = 96, kTmdQ = 192, kTmdV = 320, kTmdK = 416;
+};
+
+template <int DB>
+__global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __grid_constant__ BwdParams p) {
+  using Sh = FewKeyShape<DB>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* aligned = smem_raw + (base - smem_u32(smem_raw));
+  FewKeyBarriers* bar = reinterpret_cast<FewKeyBarriers*>(aligned + Sh::kBar);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bar->abort_flag;
+  int* err = p.status;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar->kfull, 1), mbar_init(&bar->kready, 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&bar->full[i], 1), mbar_init(&bar->empty[i], 2), mbar_init(&bar->ready[i], 1);
+    mbar_init(&bar->sfull, 1), mbar_init(&bar->sread, kSoftWarps), mbar_init(&bar->pfull, kSoftWarps);
+    mbar_init(&bar->qdone, 1), mbar_init(&bar->sdone, 1), mbar_init(&bar->fin[0], 1), mbar_init(&bar->fin[1], 1);
+    bar->abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&p.mk), prefetch_tmap(&p.mv), prefetch_tmap(&p.fq), prefetch_tmap(&p.fdo);
+  }
+  if (warp == kSumWarp) {
+    tmem_alloc(&bar->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  int item = blockIdx.x;
+  const int hk = item % p.Hkv;
+  item /= p.Hkv;
+  const int split = item % p.ksplits, g = item / p.ksplits;
+  int q0, q1, k0, k1;
+  const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
+  if (flags && threadIdx.x == 0 && split == 0 && hk == 0) atomicOr(p.status, flags);
+  const bool bad = flags & SVCONV_STATUS_BAD_OFFSETS;
+  const int ftok = kTile / p.r, mtok = kMove / p.r, tiles = bad ? 0 : (q1 - q0 + ftok - 1) / ftok, keys = bad ? 0 : k1 - k0;
+  const int t_lo = (int)((int64_t)tiles * split / p.ksplits), t_hi = (int)((int64_t)tiles * (split + 1) / p.ksplits);
+  const int nt = keys > 0 ? t_hi - t_lo : 0, tok0 = q0 + t_lo * ftok;
+  const int n16 = (p.max_kv + 15) / 16 * 16;  // columns of the scores
+  auto rows_of = [&](int t) { return min(ftok, q1 - tok0 - t * ftok) * p.r; };
+
+  int loaded = 0;
+  if (warp == kLoadWarp) {
+    if (lane == 0 && nt > 0) {
+      mbar_arrive_expect_tx(&bar->kfull, 2 * DB * kFewKeyBlock);
+      for (int b = 0; b < DB; ++b) {
+        tma_load_3d(base + b * kFewKeyBlock, &p.mk, &bar->kfull, b * 64, hk, k0);
+        tma_load_3d(base + (DB + b) * kFewKeyBlock, &p.mv, &bar->kfull, b * 64, hk, k0);
+      }
+      for (; loaded < 2 * nt; ++loaded) {
+        const int slot = loaded % NS;
+        if (loaded >= NS) wait_for(&bar->empty[slot], ((loaded / NS) & 1) ^ 1, abort_flag, err);
+        if (*abort_flag) break;
+        mbar_arrive_expect_tx(&bar->full[slot], (uint32_t)(ftok * p.r) * 128u * DB);
+        for (int b = 0; b < DB; ++b)
+          tma_load_4d(base + Sh::kRing + slot * Sh::kTileBytes + b * kBlockBytes, (loaded & 1) ? &p.fdo : &p.fq, &bar->full[slot], b * 64, 0,
+                      hk, tok0 + (loaded >> 1) * ftok);
+      }
+    }
+  } else if (warp == kScoreWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const int ks = (p.d + 15) / 16, n = uniform(nt);
+      const uint32_t idesc = idesc_bf16_f32(kTile, n16, 0, 0), tm = uniform(tmem);
+      const uint64_t dkv = smem_desc_sw128(base, 16, 1024), dq = smem_desc_sw128(base + Sh::kRing, 16, 1024);
+      // operand o (0: Q K, 1: dO V) of the tile in this slot
+      auto scores = [&](int o, int slot, uint32_t d) {
+        const uint64_t a0 = dq + (uint64_t)(slot * (Sh::kTileBytes >> 4)), b0 = dkv + (uint64_t)(o * DB * (kFewKeyBlock >> 4));
+#pragma unroll
+        for (int k = 0; k < 4 * DB; ++k)
+          if (k < ks)
+            mma_ss(d, a0 + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), b0 + (uint64_t)((k >> 2) * (kFewKeyBlock >> 4) + (k & 3) * 2),
+                   idesc, k ? 1u : 0u, e);
+      };
+      wait_warp(&bar->kready, 0, abort_flag, err);
+      for (int t = 0; t < n; ++t) {
+        const int q = 2 * t, o = q + 1;
+        wait_warp(&bar->full[q % NS], (q / NS) & 1, abort_flag, err);
+        if (t > 0) wait_warp(&bar->sread, (t - 1) & 1, abort_flag, err);  // the columns are free
+        tc_fence_after();
+        scores(0, q % NS, tm + Sh::kTmS);
+        wait_warp(&bar->full[o % NS], (o / NS) & 1, abort_flag, err);
+        tc_fence_after();
+        scores(1, o % NS, tm + Sh::kTmdP);
+        commit_to(&bar->sfull, e);
+      }
+      commit_to(&bar->fin[0], e);  // every issued product is complete before tensor memory is released
+      wait_warp(&bar->fin[0], 0, abort_flag, err);
+    }
+  } else if (warp == kSumWarp) {
+    if (nt > 0) {
+      const uint32_t e = lane == 0;
+      const int n = uniform(nt), nk = uniform(n16 / 16);
+      const uint32_t tm = uniform(tmem), idesc_q = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), idesc_s = idesc_bf16_f32(kTile, n16, 1, 1);
+      const uint64_t dk = smem_desc_sw128(base, kFewKeyBlock, 1024), dsa = smem_desc_sw128(base + Sh::kdS, 16, 1024);
+      // up to 64 channels A's second half of rows is whatever follows the tile: rows of dV^T and dK^T that are not read
+      const uint64_t dt = smem_desc_sw128(base + Sh::kRing, kBlockBytes, 1024);
+      const uint64_t dpb = smem_desc_sw128(base + Sh::kP, kBlockBytes, 1024), dsb = smem_desc_sw128(base + Sh::kdS, kBlockBytes, 1024);
+      for (int t = 0; t < n; ++t) {
+        const int sq = 2 * t % NS, so = (2 * t + 1) % NS;
+        wait_warp(&bar->pfull, t & 1, abort_flag, err);  // dQ was read by then, too
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kFewKeys / 16; ++k)
+          if (k < nk)
+            mma_ss(tm + Sh::kTmdQ, dsa + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), dk + (uint64_t)(k * (2048 >> 4)), idesc_q, k ? 1u : 0u, e);
+        commit_to(&bar->qdone, e);
+        if (rows_of(t) < kTile) {  // rows that do not exist are zero by then
+          wait_warp(&bar->ready[sq], (2 * t / NS) & 1, abort_flag, err);
+          wait_warp(&bar->ready[so], ((2 * t + 1) / NS) & 1, abort_flag, err);
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) {
+          mma_ss(tm + Sh::kTmdV, dt + (uint64_t)(so * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dpb + (uint64_t)(k * (2048 >> 4)), idesc_s, t || k ? 1u : 0u, e);
+          mma_ss(tm + Sh::kTmdK, dt + (uint64_t)(sq * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dsb + (uint64_t)(k * (2048 >> 4)), idesc_s, t || k ? 1u : 0u, e);
+        }
+        commit_to(&bar->sdone, e);
+        commit_to(&bar->empty[sq], e);
+        commit_to(&bar->empty[so], e);
+      }
+      commit_to(&bar->fin[1], e);
+      wait_warp(&bar->fin[1], 0, abort_flag, err);
+    }
+  } else if (warp == kCheckWarp) {
+    if (nt > 0) {
+      wait_warp(&bar->kfull, 0, abort_flag, err);
+      uint32_t w[4];
+      kept_words(p.keep, k0, k1, w);
+      if (lane < 4) bar->kept[lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+      const uint32_t drop[3] = {~w[0], ~w[1], ~w[2]};
+      scrub_rows(base, 2 * DB, kFewKeyBlock, drop);
+      warp_arrive(&bar->kready);
+    }
+    for (int j = 0; j < 2 * nt; ++j) {
+      const int slot = j % NS, rows = rows_of(j >> 1);
+      wait_warp(&bar->full[slot], (j / NS) & 1, abort_flag, err);
+      if (rows < kTile) {
+        uint32_t drop[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) drop[i] = rows <= 32 * i ? ~0u : rows >= 32 * i + 32 ? 0u : ~0u << (rows - 32 * i);
+        scrub_rows(base + Sh::kRing + slot * Sh::kTileBytes, DB, kBlockBytes, drop);
+      }
+      warp_arrive(&bar->ready[slot]);
+      warp_arrive(&bar->empty[slot]);
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS and dQ: four threads per query row, 24 keys each
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane, col0 = part * 24;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const f2 c2 = pack2(p.c, p.c);
+    uint32_t kept = 0;  // of this part's keys
+    if (nt > 0) {
+      wait_warp(&bar->kready, 0, abort_flag, err);
+      const uint64_t two = (uint64_t)bar->kept[col0 >> 5] | (uint64_t)bar->kept[(col0 >> 5) + 1] << 32;
+      kept = (uint32_t)(two >> (col0 & 31)) & 0xffffffu;
+    }
+    const int rq = row / p.r, rh = row - rq * p.r;  // the row's token in its tile, and head
+    // statistics of this row of tile t: -lse in base 2 and -D
+    auto stat_of = [&](int t, float& l, float& dd) {
+      if (t >= nt || row >= rows_of(t)) return;
+      const int at = (t_lo + t) * ftok + rq, tile = at / mtok;
+      const float* st = p.stat + ((int64_t)hk * p.stat_tiles + q0 / mtok + g + tile) * kStat + (at - tile * mtok) * p.r + rh;
+      l = st[0], dd = st[kMove];
+    };
+    float next_l = 0.f, next_d = 0.f;
+    stat_of(0, next_l, next_d);
+    for (int t = 0; t < nt; ++t) {
+      const bool row_on = row < rows_of(t);
+      const f2 nl = pack2(next_l, next_l), nd = pack2(next_d, next_d);
+      const uint32_t bits = row_on ? kept : 0u;
+      stat_of(t + 1, next_l, next_d);
+      wait_warp(&bar->sfull, t & 1, abort_flag, err);
+      tc_fence_after();
+      uint32_t a[3][8], b[3][8];
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (col0 + 8 * i < n16) {
+          tmem_ld_x8(tmem + lanes + Sh::kTmS + col0 + 8 * i, a[i]);
+          tmem_ld_x8(tmem + lanes + Sh::kTmdP + col0 + 8 * i, b[i]);
+        }
+      tmem_ld_wait();
+      tc_fence_before();
+      warp_arrive(&bar->sread);
+      if (t > 0) wait_warp(&bar->sdone, (t - 1) & 1, abort_flag, err);  // P and dS are free again
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int col = col0 + 8 * i;
+        if (col >= n16) continue;
+        uint32_t w[4], u[4];
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          float x, y;
+          unpack2(fma2(pack2(a[i][k], a[i][k + 1]), c2, nl), x, y);
+          x = ex2(x);
+          y = ex2(y);
+          w[k / 2] = pack_bf16(x, y);
+          unpack2(mul2(pack2(x, y), add2(pack2(b[i][k], b[i][k + 1]), nd)), x, y);
+          u[k / 2] = pack_bf16(x, y);
+        }
+        if (!__all_sync(0xffffffffu, (bits >> (8 * i) & 0xffu) == 0xffu)) {  // rows that do not exist and keys that take no part: weight 0
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t on = (bits >> (8 * i + 2 * k) & 1u ? 0xffffu : 0u) | (bits >> (8 * i + 2 * k + 1) & 1u ? 0xffff0000u : 0u);
+            w[k] &= on, u[k] &= on;
+          }
+        }
+        const uint32_t at = base + (uint32_t)((col >> 6) * kBlockBytes + row * 128 + (((col & 63) >> 3) ^ (row & 7)) * 16);
+        st_shared_16(at + Sh::kP, w[0], w[1], w[2], w[3]);
+        st_shared_16(at + Sh::kdS, u[0], u[1], u[2], u[3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bar->pfull);
+      wait_warp(&bar->qdone, t & 1, abort_flag, err);
+      tc_fence_after();
+#pragma unroll
+      for (int b2 = 0; b2 < DB; ++b2) {
+        const int c = (part * DB + b2) * 16;
+        if (c >= p.d) break;
+        uint32_t o[16];
+        tmem_ld_x16(tmem + lanes + Sh::kTmdQ + c, o);
+        tmem_ld_wait();
+        if (!row_on) continue;
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) * p.scale;
+        store_row(p.dQ + ((int64_t)(tok0 + t * ftok + rq) * p.Hq + hk * p.r + rh) * p.d + c, v, p.d - c, p.wide);
+      }
+      tc_fence_before();
+    }
+    if (nt > 0) wait_warp(&bar->fin[1], 0, abort_flag, err);
+    tc_fence_after();
+    // dV and dK: a channel a thread, 24 keys a warpgroup
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) {
+      const int key0 = (warp >> 2) * 24 + 8 * i;
+      if (key0 >= n16) break;
+      uint32_t o[8], w[8];
+      if (nt > 0) {
+        tmem_ld_x8(tmem + lanes + Sh::kTmdV + key0, o);
+        tmem_ld_x8(tmem + lanes + Sh::kTmdK + key0, w);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int key = key0 + k;
+        if (key >= keys || row >= p.d) continue;
+        const int64_t at = ((int64_t)(k0 + key) * p.Hkv + hk) * p.d + row, from = split * ((int64_t)p.nkv * p.Hkv * p.d) + at;
+        const float dv = nt > 0 ? __uint_as_float(o[k]) : 0.f, dk = nt > 0 ? __uint_as_float(w[k]) * p.scale : 0.f;
+        if (p.ksplits > 1) p.part_v[from] = dv, p.part_k[from] = dk;
+        else p.dV[at] = __float2bfloat16(dv), p.dK[at] = __float2bfloat16(dk);
+      }
+    }
+    if (keys == 0 && !bad) {  // queries without keys
+      const int64_t lo = (int64_t)tok0 * p.Hq, chunks = p.d / 8, per = (int64_t)p.r * chunks;
+      for (int64_t i = threadIdx.x; i < (min(q1, q0 + t_hi * ftok) - tok0) * per; i += kSoftWarps * 32)
+        *reinterpret_cast<uint4*>(p.dQ + (lo + i / per * p.Hq + hk * p.r) * p.d + i % per * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (bar->abort_flag && warp == kLoadWarp && lane == 0 && nt > 0) {
+    // a wait ran out somewhere: let the copies in flight land before the CTA gives its memory back
+    volatile int never = 0;
+    mbar_wait(&bar->kfull, 0, &never, err, kDefaultTimeoutNs);
+    for (int i = loaded > NS ? loaded - NS : 0; i < loaded; ++i)
+      mbar_wait(&bar->full[i % NS], (i / NS) & 1, &never, err, kDefaultTimeoutNs);
+  }
+  if (warp == kSumWarp) tmem_dealloc(tmem, 512);
+}
+
 // -lse in base 2 and -D = -dO . O of every (query token, head), 64 packed rows of a key head to a tile as the
 // key pass reads them: group g's tiles start at tile q_off[g] / tokens + g, which leaves room for each
 // group's last, partly filled one.  Rows that do not exist, and rows without any key, get -inf and 0, so
@@ -1633,9 +1937,12 @@ __global__ void __launch_bounds__(256) attn_stat_kernel(const __nv_bfloat16* __r
 // The splits of a gradient added up: 8 channels a thread over the rows of group blockIdx.y, by SLICES warps of the block
 // that take every SLICES-th split and whose sums are added in order.  One slice moves the most bytes; eight
 // shorten the chain of loads where there are many splits (148 of 32 rows: a call of 22.7 us takes 14.5).
+// blockIdx.z: the gradient (dK and dV in one launch).
 template <int SLICES>
-__global__ void __launch_bounds__(256) attn_sum_kernel(const float* __restrict__ part, int splits, const int32_t* off, const int32_t* off2,
-                                                       int n, int n2, int bound, int H, int d, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(256) attn_sum_kernel(const float* part0, const float* part1, int splits, const int32_t* off, const int32_t* off2,
+                                                       int n, int n2, int bound, int H, int d, __nv_bfloat16* out0, __nv_bfloat16* out1) {
+  const float* __restrict__ part = blockIdx.z ? part1 : part0;
+  __nv_bfloat16* __restrict__ out = blockIdx.z ? out1 : out0;
   constexpr int kThreadsX = 256 / SLICES;
   __shared__ float s_v[SLICES > 1 ? SLICES : 1][SLICES > 1 ? kThreadsX : 1][9];
   const int x = threadIdx.x % kThreadsX, y = threadIdx.x / kThreadsX;
@@ -1788,11 +2095,13 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
 // half an SM's share of all work, by that schedule's end plus the cost of the partial results.  In units of one
 // moving tile of the query pass (about 0.6 us).
 constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kBwdMerge = 5.0, kBwdMergeBytes = 3.0e6;
-// Few queries: microseconds of a key tile of 64 channels, of a CTA beside its tiles, and of adding the splits up.
-constexpr double kFewTile = 1.5, kFewFixed = 8.0, kFewMerge = 5.0;
+// Few queries or few keys: microseconds of a tile of 64 channels, of a CTA beside its tiles, and of adding the splits up.
+// Few keys under fewer than kFewItems query tiles in all stay with the two passes, whose items are shorter: 50 keys, 4
+// heads of 64, 200 queries (8 tiles) 14.5 us against 12.4, 900 (32 tiles) 16.5 each, 8 x 6,144 over 77 52 against 76.
+constexpr double kFewTile = 1.5, kFewKeyTile = 2.5, kFewFixed = 8.0, kFewMerge = 5.0, kFewItems = 24.0;
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits, keys_first;
-  int few;              // the kernel for few queries, with qsplits cuts of the keys
+  int few;              // 1: the kernel for few queries, with qsplits cuts of the keys; 2: for few keys, ksplits cuts of the queries
   int tiles;            // of statistics, for each key head
   size_t stat, pq, pk;  // floats: statistics, split partials of dQ, of dK (and again of dV)
   size_t floats() const { return stat + pq + 2 * pk; }
@@ -1848,22 +2157,28 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
       const double lq = (double)tq / sq + kBwdFixed, lk = (double)tk * kKeyTile / sk + kBwdFixed;
       const bool kf = lk > lq;
       const double t = (kf ? schedule_end(nkb * sk, lk, nqb * sq, lq) : schedule_end(nqb * sq, lq, nkb * sk, lk)) +
-                       (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? 2 * kBwdMerge + bk * sk : 0.0);
+                       (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? kBwdMerge + bk * sk : 0.0);
       if (best == 0.0 || t < best) best = t, b.qsplits = sq, b.ksplits = sk, b.keys_first = kf;
     }
-  b.few = c.max_q > 0 && c.max_kv > 0 && (int64_t)c.max_q * r <= kFew;
-  if (b.few) {  // one item a split of a group's keys and key head
-    const int tiles = cdiv(c.max_kv, kTile);
-    const double units = (double)G * c.Hkv, tile = c.d <= 64 ? kFewTile : 2 * kFewTile;
+  b.few = c.max_q == 0 || c.max_kv == 0                                                                       ? 0
+          : (int64_t)c.max_q * r <= kFew                                                                        ? 1
+          : c.max_kv <= kFewKeys && c.Hkv * blocks_est(c.nq, c.max_q, G, kTile / r) >= kFewItems ? 2
+                                                                                                                : 0;
+  if (b.few) {  // one item a split of a group's keys (queries) and key head
+    const int tiles = b.few == 1 ? cdiv(c.max_kv, kTile) : cdiv(c.max_q, kTile / r);
+    const double units = (double)G * c.Hkv, tile = (b.few == 1 ? kFewTile : kFewKeyTile) * (c.d <= 64 ? 1 : 2);
+    const double bytes = b.few == 1 ? bq : bk;
+    int splits = 1;
     best = 0.0;
-    b.ksplits = 1;
     for (int s = 1; s <= tiles && (s == 1 || units * s <= 8.0 * kSms); ++s) {
-      const double t = std::ceil(units * s / kSms) * (cdiv(tiles, s) * tile + kFewFixed) + (s > 1 ? kFewMerge + bq * s : 0.0);
-      if (best == 0.0 || t < best) best = t, b.qsplits = s;
+      const double t = std::ceil(units * s / kSms) * (cdiv(tiles, s) * tile + kFewFixed) + (s > 1 ? kFewMerge + bytes * s : 0.0);
+      if (best == 0.0 || t < best) best = t, splits = s;
     }
+    b.qsplits = b.few == 1 ? splits : 1;
+    b.ksplits = b.few == 2 ? splits : 1;
   }
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
-  b.tiles = b.few ? 0 : c.nq / (kMove / r) + c.G + 1;
+  b.tiles = b.few == 1 ? 0 : c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
   b.pq = b.qsplits > 1 ? b.qsplits * nq * c.d : 0;
   b.pk = b.ksplits > 1 ? b.ksplits * nk * c.d : 0;
@@ -1882,6 +2197,13 @@ cudaError_t launch_few(const BwdParams& p, int grid, cudaStream_t s) {
   static int done[64];
   cudaError_t e = ensure_smem_attr(attn_bwd_few_kernel<DB>, FewShape<DB>::kSmem, done);
   return e == cudaSuccess ? launch_pdl(attn_bwd_few_kernel<DB>, dim3(grid), dim3(kThreads), FewShape<DB>::kSmem, s, p) : e;
+}
+
+template <int DB>
+cudaError_t launch_few_keys(const BwdParams& p, int grid, cudaStream_t s) {
+  static int done[64];
+  cudaError_t e = ensure_smem_attr(attn_bwd_few_keys_kernel<DB>, FewKeyShape<DB>::kSmem, done);
+  return e == cudaSuccess ? launch_pdl(attn_bwd_few_keys_kernel<DB>, dim3(grid), dim3(kThreads), FewKeyShape<DB>::kSmem, s, p) : e;
 }
 
 template <int DB>
@@ -1974,7 +2296,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   if ((rc = check_device())) return rc;
   const BwdPlan b = plan_bwd(c);
   const long long heads = (long long)c.G * c.Hkv;
-  const long long q_items = heads * (b.few ? 1 : b.qblocks) * b.qsplits, k_items = b.few ? 0 : heads * b.kblocks * b.ksplits;
+  const long long q_items = heads * (b.few ? 1 : b.qblocks) * b.qsplits, k_items = heads * (b.few ? 1 : b.kblocks) * b.ksplits;
   const int r = c.Hq / c.Hkv;
   int lanes = 1;
   while (lanes < c.d / 8) lanes *= 2;
@@ -2005,33 +2327,35 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   const void *q = c.nq ? Q : K, *go = c.nq ? dO : K, *k = c.nkv ? K : Q, *v = c.nkv ? V : Q;
   const int64_t go_row = (int64_t)c.Hq * c.d, go_head = c.d;
   if (!make_packed_map(&p.fq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, kTile / r) ||
-      !make_packed_map(&p.mq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, (b.few ? kFew : kMove) / r) ||
+      !make_packed_map(&p.mq, q, c.nq, c.Hkv, r, c.d, c.q_row, c.q_head, (b.few == 1 ? kFew : kMove) / r) ||
       !make_packed_map(&p.fdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, kTile / r) ||
-      !make_packed_map(&p.mdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, (b.few ? kFew : kMove) / r) ||
+      !make_packed_map(&p.mdo, go, c.nq, c.Hkv, r, c.d, go_row, go_head, (b.few == 1 ? kFew : kMove) / r) ||
       !make_rows_map(&p.fk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kTile) ||
-      !make_rows_map(&p.mk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, kMove) ||
+      !make_rows_map(&p.mk, k, c.nkv, c.Hkv, c.d, c.k_row, c.k_head, b.few == 2 ? kFewKeys : kMove) ||
       !make_rows_map(&p.fv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kTile) ||
-      !make_rows_map(&p.mv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, kMove))
+      !make_rows_map(&p.mv, v, c.nkv, c.Hkv, c.d, c.v_row, c.v_head, b.few == 2 ? kFewKeys : kMove))
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (c.max_q > 0 && !b.few)
+  if (c.max_q > 0 && b.few != 1)
     e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid, c.G), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
                    static_cast<const __nv_bfloat16*>(O), lse, c.q_off, c.nq, c.max_q, c.Hq, c.Hkv, c.d, lanes, b.tiles, ws);
-  if (e == cudaSuccess && b.few)
+  if (e == cudaSuccess && b.few == 1)
     e = c.d <= 64 ? launch_few<1>(p, (int)q_items, s) : launch_few<2>(p, (int)q_items, s);
+  else if (e == cudaSuccess && b.few == 2)
+    e = c.d <= 64 ? launch_few_keys<1>(p, (int)k_items, s) : launch_few_keys<2>(p, (int)k_items, s);
   else if (e == cudaSuccess)
     e = c.d <= 64 ? launch_bwd<1>(p, (int)(q_items + k_items), s) : launch_bwd<2>(p, (int)(q_items + k_items), s);
-  auto add = [&](const float* part, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound, int H,
-                 __nv_bfloat16* out) {
+  auto add = [&](const float* part0, const float* part1, int splits, const int32_t* off, const int32_t* off2, int n, int n2, int bound,
+                 int H, __nv_bfloat16* out0, __nv_bfloat16* out1) {
     if (e != cudaSuccess || splits < 2) return;
     const long long chunks = (long long)bound * H * c.d / 8;
-    e = splits > 8 ? launch_pdl(attn_sum_kernel<8>, dim3((unsigned)((chunks + 31) / 32), c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out)
-                   : launch_pdl(attn_sum_kernel<1>, dim3((unsigned)((chunks + 255) / 256), c.G), dim3(256), 0, s, part, splits, off, off2, n, n2, bound, H, c.d, out);
+    const int slices = splits > 8 ? 8 : 1, per = 256 / slices;
+    e = launch_pdl(slices > 1 ? attn_sum_kernel<8> : attn_sum_kernel<1>, dim3((unsigned)((chunks + per - 1) / per), c.G, out1 ? 2 : 1), dim3(256), 0,
+                   s, part0, part1, splits, off, off2, n, n2, bound, H, c.d, out0, out1);
   };
-  add(p.part_q, b.qsplits, c.q_off, c.kv_off, c.nq, c.nkv, c.max_q, c.Hq, p.dQ);
-  add(p.part_k, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dK);
-  add(p.part_v, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dV);
+  add(p.part_q, nullptr, b.qsplits, c.q_off, c.kv_off, c.nq, c.nkv, c.max_q, c.Hq, p.dQ, nullptr);
+  add(p.part_k, p.part_v, b.ksplits, c.kv_off, c.q_off, c.nkv, c.nq, c.max_kv, c.Hkv, p.dK, p.dV);
   return e == cudaSuccess ? SVCONV_OK : SVCONV_ERR_CUDA;
 }
 

@@ -228,11 +228,43 @@ def test_few_queries(sv, i):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_few_queries_among_rows_that_hold_anything(sv, d):
-    """NaN and infinities in dropped keys and in rows of other groups and of no group, behind short query tiles."""
-    x = make(77, (5, 9), (300, 700), 2, 2, d, keep=0.6, gap=9)
+FEW_KEYS = [  # at most 96 keys a group, more than 32 query rows
+    ((700, 200), (77, 77), 4, 4, 64, 1.0, 0, False),
+    ((500,), (96,), 2, 1, 128, 1.0, 0, False),
+    ((300, 33, 0, 1), (1, 16, 17, 96), 2, 2, 64, 0.7, 2, True),
+    ((130, 257, 40), (95, 0, 33), 3, 1, 96, 0.9, 1, False),
+    ((40, 2), (5, 64), 32, 1, 128, 0.5, 3, False),
+    ((1000, 43), (7, 12), 6, 2, 40, 0.5, 0, True),
+    ((3000,), (30,), 1, 1, 8, 1.0, 0, False),
+    (tuple(range(0, 200, 5)), (50,) * 40, 4, 2, 80, 0.9, 0, False),
+    ((20000, 300), (65, 80), 2, 2, 64, 0.9, 4, False),
+    ((9000,), (81,), 5, 1, 128, 1.0, 0, False),
+]
+
+
+@pytest.mark.parametrize("i", range(len(FEW_KEYS)))
+def test_few_keys(sv, i):
+    q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused = FEW_KEYS[i]
+    x = make(80 + i, q_lens, kv_lens, Hq, Hkv, d, keep, gap, fused)
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, f"few keys {i}")
+    again = run_both(sv, x)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("d,Hq", [(64, 2), (128, 2), (64, 6), (128, 6)])
+def test_few_keys_among_rows_that_hold_anything(sv, d, Hq):
+    """The same as for few queries below, behind short key tiles and short last query tiles."""
+    x = make(78, (95, 140), (30, 70), Hq, 2, d, keep=0.6, gap=9)
     want = run_both(sv, x)
+    spoil(x)
+    got = run_both(sv, x)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+
+
+def spoil(x):
+    """NaN and infinities in dropped keys and in rows of no group."""
     qo, ko = x["q_off"].tolist(), x["kv_off"].tolist()
     out_q = torch.ones(x["Q"].shape[0], dtype=torch.bool, device="cuda")
     out_q[qo[0]:qo[-1]] = False
@@ -242,6 +274,14 @@ def test_few_queries_among_rows_that_hold_anything(sv, d):
         x[k][drop] = float("nan") if n else float("inf")
     for k in ("Q", "dO"):
         x[k][out_q] = float("nan")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_queries_among_rows_that_hold_anything(sv, d):
+    """NaN and infinities in dropped keys and in rows of other groups and of no group, behind short query tiles."""
+    x = make(77, (5, 9), (300, 700), 2, 2, d, keep=0.6, gap=9)
+    want = run_both(sv, x)
+    spoil(x)
     got = run_both(sv, x)
     for k in want:
         assert torch.equal(got[k], want[k]), k
