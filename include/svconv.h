@@ -303,8 +303,8 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *              written).  Offsets that decrease or leave 0..nq / 0..nkv set
  *              SVCONV_STATUS_BAD_OFFSETS and that group is treated as empty (nothing written).
  *   dev_status int32 device or NULL (then the library's error word takes the bits).
- *   workspace  >= svconv_cross_attn_fwd_workspace_size(desc) bytes, 16-byte aligned (may be
- *              NULL if that is 0), no initial contents required.  Calls that overlap on the GPU
+ *   workspace  >= svconv_cross_attn_fwd_workspace_size(desc) bytes (_bwd_ for the gradients),
+ *              16-byte aligned (may be NULL if that is 0), no initial contents required.  Calls that overlap on the GPU
  *              (captured graphs included) need a workspace each.
  *   Limits: d a multiple of 8, 8 <= d <= 128; Hq a multiple of Hkv, Hq / Hkv <= 64;
  *   scale finite.  Deterministic: bitwise identical results for identical calls.

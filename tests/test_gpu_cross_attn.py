@@ -413,6 +413,43 @@ def test_bad_offsets_are_flagged_and_their_groups_skipped(sv):
     assert sv.svconv_read_error_word() == 0
 
 
+@pytest.mark.parametrize("q_lens,kv_lens", [((9, 8), (300, 20)), ((700, 600), (90, 20))])
+def test_bad_offsets_and_bounds_with_few_rows(sv, q_lens, kv_lens):
+    """The backward forms for few queries and for few keys: bad groups are skipped, rows past a bound left out."""
+    x = make(17, q_lens, kv_lens, 2, 2, 64)
+    want = run_both(sv, x)
+    nq, nk = sum(q_lens), sum(kv_lens)
+
+    def bwd(q_off, kv_off, max_q, max_kv):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = [torch.full_like(x[k], 7.0) for k in ("Q", "K", "V")]
+        sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], want["O"], want["lse"], q_off, kv_off, max_q=max_q, max_kv=max_kv,
+                                 status=st, dQ=out[0], dK=out[1], dV=out[2])
+        torch.cuda.synchronize()
+        return int(st.item()), out
+
+    tens = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    a, b = q_lens[0], kv_lens[0]
+    for q_off, kv_off in (([0, a, nq], [0, b, nk + 1]), ([0, a, a - 1], [0, b, nk])):
+        flags, (dQ, dK, dV) = bwd(tens(q_off), tens(kv_off), max(q_lens), max(kv_lens))
+        assert flags == sv.STATUS_BAD_OFFSETS
+        assert torch.equal(dQ[:a], want["dQ"][:a]) and torch.equal(dK[:b], want["dK"][:b]) and torch.equal(dV[:b], want["dV"][:b])
+        assert (dQ[a:] == 7.0).all() and (dK[b:] == 7.0).all() and (dV[b:] == 7.0).all()
+    # a bound below the first group's keys: its first rows are the group (the rest is not written)
+    short = b - 7
+    flags, (dQ, dK, dV) = bwd(x["q_off"], x["kv_off"], max(q_lens), short)
+    assert flags == sv.STATUS_CHUNK_OVERFLOW
+    assert (dK[short:b] == 7.0).all() and (dV[short:b] == 7.0).all() and torch.isfinite(dQ[:a].float()).all()
+    assert torch.equal(dK[:short], want["dK"][:short]) and torch.equal(dV[:short], want["dV"][:short])
+    assert torch.equal(dK[b:], want["dK"][b:])
+    # a bound below the first group's queries
+    if a > 8:
+        flags, (dQ, dK, dV) = bwd(x["q_off"], x["kv_off"], a - 1, max(kv_lens))
+        assert flags == sv.STATUS_CHUNK_OVERFLOW
+        assert torch.equal(dQ[:a - 1], want["dQ"][:a - 1]) and (dQ[a - 1] == 7.0).all() and torch.equal(dQ[a:], want["dQ"][a:])
+    assert sv.svconv_read_error_word() == 0
+
+
 def test_streams_and_captured_graphs(sv):
     """A side stream, and two captured graphs (a workspace each) replayed on two streams."""
     xs = [make(20 + i, (33, 200), (2500, 700), 4, 2, 64) for i in range(2)]

@@ -58,9 +58,13 @@ def test_cross_attention_arguments(L):
         assert bwd(L, desc(), **{name: None}) == NULL, name
     for name in ("dO", "Q", "K", "V", "O", "dQ", "dK", "dV", "ws"):
         assert bwd(L, desc(), **{name: ODD}) == ALIGN, name
-    need = L.svconv_cross_attn_bwd_workspace_size(ctypes.byref(desc()))
-    assert need >= 8 * 4 * 4
-    assert bwd(L, desc(), ws=None) == WORKSPACE and bwd(L, desc(), n=need - 1) == WORKSPACE
+    more = desc(nq=80, max_q=80, nkv=200, max_kv=200)  # beyond one tile of either side: statistics of every row
+    need = L.svconv_cross_attn_bwd_workspace_size(ctypes.byref(more))
+    assert need >= 80 * 4 * 4
+    assert bwd(L, more, ws=None) == WORKSPACE and bwd(L, more, n=need - 1) == WORKSPACE
+    many = desc(nkv=30000, max_kv=30000)  # few queries: splits of the keys
+    need = L.svconv_cross_attn_bwd_workspace_size(ctypes.byref(many))
+    assert need > 0 and bwd(L, many, n=need - 1) == WORKSPACE
     # nothing to do: accepted without pointers
     assert fwd(L, desc(G=0, q_off=None, kv_off=None), Q=None, O=None) == 0
     assert fwd(L, desc(max_q=0), Q=None, O=None) == 0
