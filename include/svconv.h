@@ -311,6 +311,7 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *
  * svconv_cross_attn_bwd: with dO [nq][Hq][d] bf16 and O, lse of the forward call,
  *     dP = dO V^T,  D[i] = dO[i] . O[i],  dS = P * (dP - D),
+ *   (where max_kv <= 96, D[i] = sum_j P[i][j] dP[i][j], the same without O's rounding)
  *     dQ = scale dS K,  dK = scale sum over the r query heads of dS^T Q,  dV = the same of P^T dO
  *   into dQ [nq][Hq][d], dK and dV [nkv][Hkv][d] bf16 (contiguous, overwritten; rows of dropped
  *   keys get 0).  Overlapping outputs are not allowed.  No atomics: deterministic.

@@ -921,7 +921,7 @@ struct BwdParams {
   int wide;                      // rows of the gradients start on 32-byte boundaries
   const float* stat;             // [Hkv][stat_tiles][kStat], see attn_stat_kernel
   int stat_tiles;
-  const __nv_bfloat16 *dO, *O;   // few queries: the kernel takes the statistics itself
+  const __nv_bfloat16 *dO, *O;   // few queries or keys: the kernels take the statistics themselves
   const float* lse;
   __nv_bfloat16 *dQ, *dK, *dV;
   float *part_q, *part_k, *part_v;  // [splits][rows][d] where a pass is split
@@ -1594,9 +1594,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
 
 // ---------------------------------------------------------------------------- backward, few keys
 // Groups of at most 96 keys (an encoder's states, a handful of landmarks) under many queries: the keys stay in shared
-// memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 52 us
-// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 116 against 147).
+// memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 42 us
+// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 93 against 147; 200 over 50: 12.4 each).
 //     S = Q K^T, dP = dO V^T;  dQ = dS K, written as it comes;  dV^T += dO^T P, dK^T += Q^T dS
+// A row's keys are all here, so D is the sum of P dP itself: no product with O, and none of its rounding, which would
+// show where few keys leave dP - D small.
 // P and dS go to shared memory, a row per query: K-major as the A operand of dQ, MN-major as the B operands of the sums,
 // whose A operands are the query tiles read MN-major.  Four threads share a query row, so that few registers hold a tile;
 // two groups of warps on alternate tiles gained 4% at 64 channels and lost 15% at 128, where P and dS have one place.
@@ -1606,6 +1608,7 @@ constexpr int kFewKeyBlock = kFewKeys * 128;  // bytes of a 64-channel block of 
 struct FewKeyBarriers {
   uint64_t kfull, kready, full[8], empty[8], ready[8], sfull, sread, pfull, qdone, sdone, fin[2];
   uint32_t kept[4];
+  float rowsum[2][4][kTile];  // [tile parity][quarter of the keys][row]: parts of D
   uint32_t tmem;
   int abort_flag;
 };
@@ -1659,7 +1662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
   const int flags = group_range(p.q_off, g, p.nq, p.max_q, q0, q1) | group_range(p.kv_off, g, p.nkv, p.max_kv, k0, k1);
   if (flags && threadIdx.x == 0 && split == 0 && hk == 0) atomicOr(p.status, flags);
   const bool bad = flags & SVCONV_STATUS_BAD_OFFSETS;
-  const int ftok = kTile / p.r, mtok = kMove / p.r, tiles = bad ? 0 : (q1 - q0 + ftok - 1) / ftok, keys = bad ? 0 : k1 - k0;
+  const int ftok = kTile / p.r, tiles = bad ? 0 : (q1 - q0 + ftok - 1) / ftok, keys = bad ? 0 : k1 - k0;
   const int t_lo = (int)((int64_t)tiles * split / p.ksplits), t_hi = (int)((int64_t)tiles * (split + 1) / p.ksplits);
   const int nt = keys > 0 ? t_hi - t_lo : 0, tok0 = q0 + t_lo * ftok;
   const int n16 = (p.max_kv + 15) / 16 * 16;  // columns of the scores
@@ -1782,20 +1785,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
       kept = (uint32_t)(two >> (col0 & 31)) & 0xffffffu;
     }
     const int rq = row / p.r, rh = row - rq * p.r;  // the row's token in its tile, and head
-    // statistics of this row of tile t: -lse in base 2 and -D
-    auto stat_of = [&](int t, float& l, float& dd) {
-      if (t >= nt || row >= rows_of(t)) return;
-      const int at = (t_lo + t) * ftok + rq, tile = at / mtok;
-      const float* st = p.stat + ((int64_t)hk * p.stat_tiles + q0 / mtok + g + tile) * kStat + (at - tile * mtok) * p.r + rh;
-      l = st[0], dd = st[kMove];
+    // -lse in base 2 of this row of tile t
+    auto lse_of = [&](int t) {
+      if (t >= nt || row >= rows_of(t)) return 0.f;
+      const float l = p.lse[(int64_t)(tok0 + t * ftok + rq) * p.Hq + hk * p.r + rh];
+      return l == -INFINITY ? -INFINITY : -l * kLog2e;
     };
-    float next_l = 0.f, next_d = 0.f;
-    stat_of(0, next_l, next_d);
+    float next_l = lse_of(0);
     for (int t = 0; t < nt; ++t) {
       const bool row_on = row < rows_of(t);
-      const f2 nl = pack2(next_l, next_l), nd = pack2(next_d, next_d);
+      const f2 nl = pack2(next_l, next_l);
       const uint32_t bits = row_on ? kept : 0u;
-      stat_of(t + 1, next_l, next_d);
+      next_l = lse_of(t + 1);
       wait_warp(&bar->sfull, t & 1, abort_flag, err);
       tc_fence_after();
       uint32_t a[3][8], b[3][8];
@@ -1808,6 +1809,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
       tmem_ld_wait();
       tc_fence_before();
       warp_arrive(&bar->sread);
+      // P, and this part of D = sum P dP, which the row's four threads share
+      f2 dsum = 0ull;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (col0 + 8 * i >= n16) continue;
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          float x, y;
+          unpack2(fma2(pack2(a[i][k], a[i][k + 1]), c2, nl), x, y);
+          a[i][k] = __float_as_uint(ex2(x));
+          a[i][k + 1] = __float_as_uint(ex2(y));
+        }
+        if (!__all_sync(0xffffffffu, (bits >> (8 * i) & 0xffu) == 0xffu)) {  // rows that do not exist and keys that take no part: weight 0
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (!(bits >> (8 * i + k) & 1u)) a[i][k] = b[i][k] = 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) dsum = fma2(pack2(a[i][k], a[i][k + 1]), pack2(b[i][k], b[i][k + 1]), dsum);
+      }
+      float x, y;
+      unpack2(dsum, x, y);
+      bar->rowsum[t & 1][part][row] = x + y;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + (warp & 3)) : "memory");
+      const float dd = -((bar->rowsum[t & 1][0][row] + bar->rowsum[t & 1][1][row]) + (bar->rowsum[t & 1][2][row] + bar->rowsum[t & 1][3][row]));
+      const f2 nd = pack2(dd, dd);
       if (t > 0) wait_warp(&bar->sdone, (t - 1) & 1, abort_flag, err);  // P and dS are free again
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
@@ -1816,20 +1843,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
         uint32_t w[4], u[4];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-          float x, y;
-          unpack2(fma2(pack2(a[i][k], a[i][k + 1]), c2, nl), x, y);
-          x = ex2(x);
-          y = ex2(y);
-          w[k / 2] = pack_bf16(x, y);
-          unpack2(mul2(pack2(x, y), add2(pack2(b[i][k], b[i][k + 1]), nd)), x, y);
+          w[k / 2] = pack_bf16(__uint_as_float(a[i][k]), __uint_as_float(a[i][k + 1]));
+          unpack2(mul2(pack2(a[i][k], a[i][k + 1]), add2(pack2(b[i][k], b[i][k + 1]), nd)), x, y);
           u[k / 2] = pack_bf16(x, y);
-        }
-        if (!__all_sync(0xffffffffu, (bits >> (8 * i) & 0xffu) == 0xffu)) {  // rows that do not exist and keys that take no part: weight 0
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t on = (bits >> (8 * i + 2 * k) & 1u ? 0xffffu : 0u) | (bits >> (8 * i + 2 * k + 1) & 1u ? 0xffff0000u : 0u);
-            w[k] &= on, u[k] &= on;
-          }
         }
         const uint32_t at = base + (uint32_t)((col >> 6) * kBlockBytes + row * 128 + (((col & 63) >> 3) ^ (row & 7)) * 16);
         st_shared_16(at + Sh::kP, w[0], w[1], w[2], w[3]);
@@ -2096,9 +2112,7 @@ FwdPlan plan_fwd(const svconv_cross_attn_desc& c) {
 // moving tile of the query pass (about 0.6 us).
 constexpr double kBwdFixed = 5.0, kKeyTile = 1.3, kBwdMerge = 5.0, kBwdMergeBytes = 3.0e6;
 // Few queries or few keys: microseconds of a tile of 64 channels, of a CTA beside its tiles, and of adding the splits up.
-// Few keys under fewer than kFewItems query tiles in all stay with the two passes, whose items are shorter: 50 keys, 4
-// heads of 64, 200 queries (8 tiles) 14.5 us against 12.4, 900 (32 tiles) 16.5 each, 8 x 6,144 over 77 52 against 76.
-constexpr double kFewTile = 1.5, kFewKeyTile = 2.5, kFewFixed = 8.0, kFewMerge = 5.0, kFewItems = 24.0;
+constexpr double kFewTile = 1.5, kFewKeyTile = 2.5, kFewFixed = 8.0, kFewMerge = 5.0;
 struct BwdPlan {
   int qblocks, qsplits, kblocks, ksplits, keys_first;
   int few;              // 1: the kernel for few queries, with qsplits cuts of the keys; 2: for few keys, ksplits cuts of the queries
@@ -2160,10 +2174,7 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
                        (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? kBwdMerge + bk * sk : 0.0);
       if (best == 0.0 || t < best) best = t, b.qsplits = sq, b.ksplits = sk, b.keys_first = kf;
     }
-  b.few = c.max_q == 0 || c.max_kv == 0                                                                       ? 0
-          : (int64_t)c.max_q * r <= kFew                                                                        ? 1
-          : c.max_kv <= kFewKeys && c.Hkv * blocks_est(c.nq, c.max_q, G, kTile / r) >= kFewItems ? 2
-                                                                                                                : 0;
+  b.few = c.max_q == 0 || c.max_kv == 0 ? 0 : c.max_kv <= kFewKeys ? 2 : (int64_t)c.max_q * r <= kFew ? 1 : 0;
   if (b.few) {  // one item a split of a group's keys (queries) and key head
     const int tiles = b.few == 1 ? cdiv(c.max_kv, kTile) : cdiv(c.max_q, kTile / r);
     const double units = (double)G * c.Hkv, tile = (b.few == 1 ? kFewTile : kFewKeyTile) * (c.d <= 64 ? 1 : 2);
@@ -2178,7 +2189,7 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
     b.ksplits = b.few == 2 ? splits : 1;
   }
   const size_t nq = (size_t)c.nq * c.Hq, nk = (size_t)c.nkv * c.Hkv;
-  b.tiles = b.few == 1 ? 0 : c.nq / (kMove / r) + c.G + 1;
+  b.tiles = b.few ? 0 : c.nq / (kMove / r) + c.G + 1;
   b.stat = (size_t)b.tiles * c.Hkv * kStat;
   b.pq = b.qsplits > 1 ? b.qsplits * nq * c.d : 0;
   b.pk = b.ksplits > 1 ? b.ksplits * nk * c.d : 0;
@@ -2337,7 +2348,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
     return SVCONV_ERR_CUDA;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
-  if (c.max_q > 0 && b.few != 1)
+  if (c.max_q > 0 && !b.few)
     e = launch_pdl(attn_stat_kernel, dim3((unsigned)stat_grid, c.G), dim3(256), 0, s, static_cast<const __nv_bfloat16*>(dO),
                    static_cast<const __nv_bfloat16*>(O), lse, c.q_off, c.nq, c.max_q, c.Hq, c.Hkv, c.d, lanes, b.tiles, ws);
   if (e == cudaSuccess && b.few == 1)

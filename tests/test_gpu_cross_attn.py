@@ -435,13 +435,26 @@ def test_bad_offsets_and_bounds_with_few_rows(sv, q_lens, kv_lens):
         assert flags == sv.STATUS_BAD_OFFSETS
         assert torch.equal(dQ[:a], want["dQ"][:a]) and torch.equal(dK[:b], want["dK"][:b]) and torch.equal(dV[:b], want["dV"][:b])
         assert (dQ[a:] == 7.0).all() and (dK[b:] == 7.0).all() and (dV[b:] == 7.0).all()
-    # a bound below the first group's keys: its first rows are the group (the rest is not written)
+    # a bound below the first group's keys, for the forward pass as well (a row's weights add up to 1 over the keys that
+    # take part): the rest is not written, and the results are those of a mask over it
     short = b - 7
+    y = dict(x)
+    y["keep"] = torch.ones(nk, dtype=torch.uint8, device="cuda")
+    y["keep"][short:b] = 0
+    ref, tol = reference(y, 0.125)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    full = want
+    want = dict(want)
+    want["O"], want["lse"] = sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], max_q=max(q_lens), max_kv=short,
+                                                      status=st)
     flags, (dQ, dK, dV) = bwd(x["q_off"], x["kv_off"], max(q_lens), short)
-    assert flags == sv.STATUS_CHUNK_OVERFLOW
-    assert (dK[short:b] == 7.0).all() and (dV[short:b] == 7.0).all() and torch.isfinite(dQ[:a].float()).all()
-    assert torch.equal(dK[:short], want["dK"][:short]) and torch.equal(dV[:short], want["dV"][:short])
-    assert torch.equal(dK[b:], want["dK"][b:])
+    assert flags == sv.STATUS_CHUNK_OVERFLOW == int(st.item())
+    assert (dK[short:b] == 7.0).all() and (dV[short:b] == 7.0).all()
+    on = y["keep"] != 0
+    for k, got in (("dK", dK[on]), ("dV", dV[on])):
+        close(got, ref[k][on], tol[k][on], f"bounded {k}")
+    close(dQ, ref["dQ"], tol["dQ"], "bounded dQ")
+    want = full
     # a bound below the first group's queries
     if a > 8:
         flags, (dQ, dK, dV) = bwd(x["q_off"], x["kv_off"], a - 1, max(kv_lens))
