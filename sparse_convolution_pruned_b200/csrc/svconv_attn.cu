@@ -1777,17 +1777,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
     // ------------------------------------------------------------ P, dS and dQ: four threads per query row, 24 keys each
     const int part = warp >> 2, row = (warp & 3) * 32 + lane, col0 = part * 24;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const f2 c2 = pack2(p.c, p.c);
     uint32_t kept = 0;  // of this part's keys
+    bool lone = false;  // a single key has weight 1 and dS = 0, exactly
     if (nt > 0) {
       wait_warp(&bar->kready, 0, abort_flag, err);
       const uint64_t two = (uint64_t)bar->kept[col0 >> 5] | (uint64_t)bar->kept[(col0 >> 5) + 1] << 32;
       kept = (uint32_t)(two >> (col0 & 31)) & 0xffffffu;
+      lone = __popc(bar->kept[0]) + __popc(bar->kept[1]) + __popc(bar->kept[2]) == 1;
     }
+    const f2 c2 = lone ? 0ull : pack2(p.c, p.c);
     const int rq = row / p.r, rh = row - rq * p.r;  // the row's token in its tile, and head
     // -lse in base 2 of this row of tile t
     auto lse_of = [&](int t) {
-      if (t >= nt || row >= rows_of(t)) return 0.f;
+      if (t >= nt || row >= rows_of(t) || lone) return 0.f;
       const float l = p.lse[(int64_t)(tok0 + t * ftok + rq) * p.Hq + hk * p.r + rh];
       return l == -INFINITY ? -INFINITY : -l * kLog2e;
     };

@@ -252,6 +252,16 @@ def test_few_keys(sv, i):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 2), (128, 6, 2), (40, 1, 1)])
+def test_a_single_key_has_no_score_gradient(sv, d, Hq, Hkv):
+    """Groups of one key, or of one that is kept: weight 1 whatever the score, so dQ and dK are exactly 0."""
+    x = make(79, (40, 7, 300), (1, 5, 1), Hq, Hkv, d)
+    x["keep"] = torch.tensor([1, 0, 0, 0, 1, 0, 1], dtype=torch.uint8, device="cuda")
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, "single keys")
+    assert (got["dQ"] == 0).all() and (got["dK"] == 0).all()
+
+
 @pytest.mark.parametrize("d,Hq", [(64, 2), (128, 2), (64, 6), (128, 6)])
 def test_few_keys_among_rows_that_hold_anything(sv, d, Hq):
     """The same as for few queries below, behind short key tiles and short last query tiles."""
