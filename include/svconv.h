@@ -292,7 +292,8 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *     S[i][j] = scale * Q[i][h] . K[j][h / r]     over the group's kept keys j
  *     P = softmax_j(S),   O[i][h] = sum_j P[i][j] V[j][h / r],   lse[i][h] = log sum_j exp(S[i][j])
  * A row whose group has no kept key gets O = 0 and lse = -inf.  The scores, the softmax's
- * statistics and all sums are fp32; P (and dS below) are rounded to bf16 as matrix operands.
+ * statistics and all sums are fp32; P (and dS below) are rounded to bf16 as matrix operands (dS to
+ * two bf16 values where a group has at most 64 keys or 32 query rows, tokens x heads of a key head).
  *   Q [nq][Hq][d], K and V [nkv][Hkv][d] bf16 with the given row and head strides (in
  *   elements, multiples of 8; channels contiguous), 16-byte aligned; O [nq][Hq][d] bf16 and
  *   lse [nq][Hq] fp32, contiguous.  kv_keep [nkv] or NULL: keys with a zero byte are left out,

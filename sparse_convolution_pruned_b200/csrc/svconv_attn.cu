@@ -191,6 +191,11 @@ __device__ __forceinline__ void commit_to(uint64_t* bar, uint32_t e) {
       : "memory");
 }
 
+// What rounding a pair to bf16 left behind, as bf16 again
+__device__ __forceinline__ uint32_t rest_bf16(float lo, float hi, uint32_t rounded) {
+  return pack_bf16(lo - __uint_as_float(rounded << 16), hi - __uint_as_float(rounded & 0xffff0000u));
+}
+
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -1277,6 +1282,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 // For the last one dS^T goes to shared memory too, one row per key, which makes it an MN-major B operand, and K's
 // tile is read as an MN-major A.  The tile's statistics (-lse in base 2 and -D of its rows) are taken in the kernel: a
 // launch before it costs more.  Two streams take alternate key tiles; at 128 channels they share the accumulators.
+// dS goes into its products as two bf16 values, the second in the unused half of each shared-memory row: a few dozen
+// scores average no rounding out (one value: dQ and dK of 13 queries over 107 keys 1.5 times as far off).
 constexpr int kFew = 32;
 constexpr int kFewBlock = kFew * 128;  // bytes of the tile's 64-channel block
 
@@ -1300,7 +1307,7 @@ struct FewShape {
   static constexpr int dS(int s) { return s * kStride + 80; }
   static constexpr int dV(int s) { return DB == 1 ? s * kStride + 96 : 192; }
   static constexpr int dK(int s) { return DB == 1 ? s * kStride + 160 : 320; }
-  static constexpr int kQ = 448;  // dQ^T: a channel a lane, a packed row a column
+  static constexpr int kQ = 448;  // dQ^T: a channel a lane, a packed row a column; from dS's second values 32 columns on
 };
 
 template <int DB>
@@ -1405,10 +1412,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
     if (nt > 0) {
       const uint32_t e = lane == 0;
       const int n = uniform(nt);
-      const uint32_t tm = uniform(tmem), idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), idesc_q = idesc_bf16_f32(kTile, kFew, 1, 1);
+      const uint32_t tm = uniform(tmem), idesc = idesc_bf16_f32(kTile, (p.d + 15) / 16 * 16, 0, 1), idesc_q = idesc_bf16_f32(kTile, 2 * kFew, 1, 1);
       const uint64_t dq = smem_desc_sw128(base, kFewBlock, 1024), dgo = smem_desc_sw128(base + DB * kFewBlock, kFewBlock, 1024);
       // up to 64 channels A's second half of rows is the next slot's V tile: rows of dQ^T that are not read
       const uint64_t dk = smem_desc_sw128(base + Sh::kRing, kBlockBytes, 1024), dds = smem_desc_sw128(base + Sh::kdS, kBlockBytes, 1024);
+      const uint64_t dsa = smem_desc_sw128(base + Sh::kdS + kFew * 2, 16, 1024);  // the second values as an A operand
       for (int t = 0; t < n; ++t) {
         const int s = t & 1, i = t >> 1, slot = 2 * t % NS;
         wait_warp(&bar->pfull[s], i & 1, abort_flag, err);
@@ -1419,6 +1427,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
           mma_ts(tm + Sh::dV(s), tm + Sh::P(s) + k * 8, dgo + (uint64_t)(k * (2048 >> 4)), idesc, k ? 1u : 0u, e);
           mma_ts(tm + Sh::dK(s), tm + Sh::dS(s) + k * 8, dq + (uint64_t)(k * (2048 >> 4)), idesc, k ? 1u : 0u, e);
         }
+#pragma unroll
+        for (int k = 0; k < kFew / 16; ++k)
+          mma_ss(tm + Sh::dK(s), dsa + (uint64_t)(s * (kBlockBytes >> 4) + k * 2), dq + (uint64_t)(k * (2048 >> 4)), idesc, 1u, e);
         commit_to(&bar->adone[s], e);
         if (partial(t)) wait_warp(&bar->kready[slot], (2 * t / NS) & 1, abort_flag, err);  // keys that take no part are zero
         tc_fence_after();
@@ -1487,7 +1498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
       const int i = t >> 1, slot = 2 * t % NS;
       wait_warp(&bar->sfull[s], i & 1, abort_flag, err);
       tc_fence_after();
-      uint32_t a[16], b[16], w[8], u[8];
+      uint32_t a[16], b[16], w[8], u[8], r[8];
       tmem_ld_x16(tmem + lanes + Sh::S(s) + h * 16, a);
       tmem_ld_x16(tmem + lanes + Sh::dP(s) + h * 16, b);
       tmem_ld_wait();
@@ -1506,13 +1517,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
           w[(k + j) / 2] = pack_bf16(x, y);
           unpack2(mul2(pack2(x, y), add2(pack2(b[k + j], b[k + j + 1]), j ? nd.y : nd.x)), x, y);
           u[(k + j) / 2] = pack_bf16(x, y);
+          r[(k + j) / 2] = rest_bf16(x, y, u[(k + j) / 2]);
         }
       }
       if (partial(t)) {
         wait_warp(&bar->kready[slot], (2 * t / NS) & 1, abort_flag, err);
         if (!(bar->kept[slot][warp & 3] >> lane & 1u)) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = u[k] = 0u;
+          for (int k = 0; k < 8; ++k) w[k] = u[k] = r[k] = 0u;
         }
       }
       tmem_st_x8(tmem + lanes + Sh::P(s) + h * 8, w);
@@ -1521,6 +1533,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
       const uint32_t ds = base + Sh::kdS + s * kBlockBytes + row * 128;
       st_shared_16(ds + ((h * 2) ^ (row & 7)) * 16, u[0], u[1], u[2], u[3]);
       st_shared_16(ds + ((h * 2 + 1) ^ (row & 7)) * 16, u[4], u[5], u[6], u[7]);
+      st_shared_16(ds + ((4 + h * 2) ^ (row & 7)) * 16, r[0], r[1], r[2], r[3]);
+      st_shared_16(ds + ((5 + h * 2) ^ (row & 7)) * 16, r[4], r[5], r[6], r[7]);
       fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
@@ -1557,9 +1571,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
     // dQ: 8 packed rows a warpgroup, a channel a thread
     if (rows > 0) {
       const int part = warp >> 2;
-      uint32_t o[8];
+      uint32_t o[8], o2[8];
       if (nt > 0) {
         tmem_ld_x8(tmem + lanes + Sh::kQ + part * 8, o);
+        tmem_ld_x8(tmem + lanes + Sh::kQ + kFew + part * 8, o2);
         tmem_ld_wait();
       }
 #pragma unroll
@@ -1567,7 +1582,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
         const int q = part * 8 + k;
         if (q >= rows || row >= p.d) continue;
         const int64_t at = ((int64_t)(q0 + q / p.r) * p.Hq + hk * p.r + q % p.r) * p.d + row;
-        const float v = nt > 0 ? __uint_as_float(o[k]) * p.scale : 0.f;
+        const float v = nt > 0 ? (__uint_as_float(o[k]) + __uint_as_float(o2[k])) * p.scale : 0.f;
         if (p.qsplits > 1) p.part_q[split * ((int64_t)p.nq * p.Hq * p.d) + at] = v;
         else p.dQ[at] = __float2bfloat16(v);
       }
@@ -1595,10 +1610,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
 // ---------------------------------------------------------------------------- backward, few keys
 // Groups of at most 96 keys (an encoder's states, a handful of landmarks) under many queries: the keys stay in shared
 // memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 42 us
-// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 93 against 147; 200 over 50: 12.4 each).
+// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 93 against 147; 200 over 50: 14.5 against 12.4).
 //     S = Q K^T, dP = dO V^T;  dQ = dS K, written as it comes;  dV^T += dO^T P, dK^T += Q^T dS
 // A row's keys are all here, so D is the sum of P dP itself: no product with O, and none of its rounding, which would
-// show where few keys leave dP - D small.
+// show where few keys leave dP - D small.  With at most 64 keys dS goes into its products as two bf16 values, the
+// second in its second block of shared memory, since so few scores average no rounding out.
 // P and dS go to shared memory, a row per query: K-major as the A operand of dQ, MN-major as the B operands of the sums,
 // whose A operands are the query tiles read MN-major.  Four threads share a query row, so that few registers hold a tile;
 // two groups of warps on alternate tiles gained 4% at 64 channels and lost 15% at 128, where P and dS have one place.
@@ -1623,7 +1639,7 @@ struct FewKeyShape {
   static constexpr int kTmS = 0, kTmdP = 96, kTmdQ = 192, kTmdV = 320, kTmdK = 416;
 };
 
-template <int DB>
+template <int DB, bool TWO>  // TWO: at most 64 keys, dS in two values
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __grid_constant__ BwdParams p) {
   using Sh = FewKeyShape<DB>;
   constexpr int NS = Sh::kStages;
@@ -1733,6 +1749,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
         for (int k = 0; k < kFewKeys / 16; ++k)
           if (k < nk)
             mma_ss(tm + Sh::kTmdQ, dsa + (uint64_t)((k >> 2) * (kBlockBytes >> 4) + (k & 3) * 2), dk + (uint64_t)(k * (2048 >> 4)), idesc_q, k ? 1u : 0u, e);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < nk) mma_ss(tm + Sh::kTmdQ, dsa + (uint64_t)((kBlockBytes >> 4) + k * 2), dk + (uint64_t)(k * (2048 >> 4)), idesc_q, 1u, e);
+        }
         commit_to(&bar->qdone, e);
         if (rows_of(t) < kTile) {  // rows that do not exist are zero by then
           wait_warp(&bar->ready[sq], (2 * t / NS) & 1, abort_flag, err);
@@ -1743,6 +1764,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
         for (int k = 0; k < kTile / 16; ++k) {
           mma_ss(tm + Sh::kTmdV, dt + (uint64_t)(so * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dpb + (uint64_t)(k * (2048 >> 4)), idesc_s, t || k ? 1u : 0u, e);
           mma_ss(tm + Sh::kTmdK, dt + (uint64_t)(sq * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dsb + (uint64_t)(k * (2048 >> 4)), idesc_s, t || k ? 1u : 0u, e);
+        }
+        if constexpr (TWO) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ss(tm + Sh::kTmdK, dt + (uint64_t)(sq * (Sh::kTileBytes >> 4) + k * (2048 >> 4)), dsb + (uint64_t)((kBlockBytes >> 4) + k * (2048 >> 4)),
+                   idesc_s, 1u, e);
         }
         commit_to(&bar->sdone, e);
         commit_to(&bar->empty[sq], e);
@@ -1781,8 +1808,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
     bool lone = false;  // a single key has weight 1 and dS = 0, exactly
     if (nt > 0) {
       wait_warp(&bar->kready, 0, abort_flag, err);
-      const uint64_t two = (uint64_t)bar->kept[col0 >> 5] | (uint64_t)bar->kept[(col0 >> 5) + 1] << 32;
-      kept = (uint32_t)(two >> (col0 & 31)) & 0xffffffu;
+      const uint64_t pair = (uint64_t)bar->kept[col0 >> 5] | (uint64_t)bar->kept[(col0 >> 5) + 1] << 32;
+      kept = (uint32_t)(pair >> (col0 & 31)) & 0xffffffu;
       lone = __popc(bar->kept[0]) + __popc(bar->kept[1]) + __popc(bar->kept[2]) == 1;
     }
     const f2 c2 = lone ? 0ull : pack2(p.c, p.c);
@@ -1842,16 +1869,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
       for (int i = 0; i < 3; ++i) {
         const int col = col0 + 8 * i;
         if (col >= n16) continue;
-        uint32_t w[4], u[4];
+        uint32_t w[4], u[4], rest[4];
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
           w[k / 2] = pack_bf16(__uint_as_float(a[i][k]), __uint_as_float(a[i][k + 1]));
           unpack2(mul2(pack2(a[i][k], a[i][k + 1]), add2(pack2(b[i][k], b[i][k + 1]), nd)), x, y);
           u[k / 2] = pack_bf16(x, y);
+          if constexpr (TWO) rest[k / 2] = rest_bf16(x, y, u[k / 2]);
         }
         const uint32_t at = base + (uint32_t)((col >> 6) * kBlockBytes + row * 128 + (((col & 63) >> 3) ^ (row & 7)) * 16);
         st_shared_16(at + Sh::kP, w[0], w[1], w[2], w[3]);
         st_shared_16(at + Sh::kdS, u[0], u[1], u[2], u[3]);
+        if constexpr (TWO) st_shared_16(at + Sh::kdS + kBlockBytes, rest[0], rest[1], rest[2], rest[3]);
       }
       fence_proxy_async_smem();
       warp_arrive(&bar->pfull);
@@ -2214,9 +2243,11 @@ cudaError_t launch_few(const BwdParams& p, int grid, cudaStream_t s) {
 
 template <int DB>
 cudaError_t launch_few_keys(const BwdParams& p, int grid, cudaStream_t s) {
-  static int done[64];
-  cudaError_t e = ensure_smem_attr(attn_bwd_few_keys_kernel<DB>, FewKeyShape<DB>::kSmem, done);
-  return e == cudaSuccess ? launch_pdl(attn_bwd_few_keys_kernel<DB>, dim3(grid), dim3(kThreads), FewKeyShape<DB>::kSmem, s, p) : e;
+  static int done[2][64];
+  const bool two = p.max_kv <= 64;
+  auto kernel = two ? attn_bwd_few_keys_kernel<DB, true> : attn_bwd_few_keys_kernel<DB, false>;
+  cudaError_t e = ensure_smem_attr(kernel, FewKeyShape<DB>::kSmem, done[two]);
+  return e == cudaSuccess ? launch_pdl(kernel, dim3(grid), dim3(kThreads), FewKeyShape<DB>::kSmem, s, p) : e;
 }
 
 template <int DB>

@@ -252,6 +252,20 @@ def test_few_keys(sv, i):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,H,d", [((13,), (107,), 4, 80), ((7, 7, 7), (22, 3, 9), 1, 32), ((6,) * 5, (3,) * 5, 2, 80),
+                                                ((2, 30), (400, 200), 2, 128), ((100,), (64,), 2, 128)])
+def test_few_rows_lose_nothing_but_the_last_rounding(sv, q_lens, kv_lens, H, d):
+    """dS enters its products with 16 bits of significand, so dQ and dK are off by their own rounding: in norm at most
+    u / sqrt(3) (a rounding is uniform within half a step), where one bf16 value for dS adds as much again.  D = dO . O with
+    the rounded O adds a part of it that falls with the number of keys: 5%."""
+    x = make(90 + d + H, q_lens, kv_lens, H, H, d)
+    got = run_both(sv, x, backward=True)
+    ref, _ = reference(x, d ** -0.5)
+    for k in ("dQ", "dK"):
+        off = float((got[k].double() - ref[k]).norm() / ref[k].norm())
+        assert off <= 1.05 * U / math.sqrt(3), (k, off)
+
+
 @pytest.mark.parametrize("d,Hq,Hkv", [(64, 2, 2), (128, 6, 2), (40, 1, 1)])
 def test_a_single_key_has_no_score_gradient(sv, d, Hq, Hkv):
     """Groups of one key, or of one that is kept: weight 1 whatever the score, so dQ and dK are exactly 0."""
@@ -497,4 +511,31 @@ def test_streams_and_captured_graphs(sv):
     for o, w in zip(outs, want):
         for k in w:
             assert torch.equal(o[k], w[k]), k
+    assert sv.svconv_read_error_word() == 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [((9, 8), (3000, 20)), ((2000, 600), (90, 20))])
+def test_captured_backward_with_few_rows(sv, q_lens, kv_lens):
+    """The backward forms for few queries and for few keys in a captured graph, replayed after the inputs changed."""
+    x = make(18, q_lens, kv_lens, 2, 2, 64)
+    kw = dict(max_q=max(q_lens), max_kv=max(kv_lens))
+
+    def step():
+        O, lse = sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], **kw)
+        return sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], O, lse, x["q_off"], x["kv_off"], **kw)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = step()
+    for name in ("Q", "V", "dO"):
+        x[name].mul_(-1.5)
+        g.replay()
+        torch.cuda.synchronize()
+        want = run_both(sv, x)
+        for k, t in zip(("dQ", "dK", "dV"), got):
+            assert torch.equal(t, want[k]), (name, k)
     assert sv.svconv_read_error_word() == 0
