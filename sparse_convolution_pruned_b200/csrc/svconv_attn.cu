@@ -949,12 +949,14 @@ struct BwdShape {
 };
 
 // Tensor-memory columns.  P and dS have columns of their own except in the key pass at 128
-// channels, where the accumulators leave room for the scores alone and P, dS take their place.
+// channels, where the accumulators leave room for the scores alone and P, dS take their place: a row's two threads
+// load 32 columns of scores each at their own pace, so each packs its 16 columns into its own 32 (kHalf).
 template <int DB, bool KEYS>
 struct BwdTmem {
   static constexpr bool kShared = DB == 2 && KEYS;
   static constexpr bool kEarly = !kShared;
   static constexpr int kStride = DB == 1 ? 192 : KEYS ? 128 : 160;
+  static constexpr int kHalf = kShared ? 32 : 16;  // columns from the first thread's part of P or dS to the second's
   static constexpr int S(int s) { return s * kStride; }
   static constexpr int dP(int s) { return s * kStride + 64; }
   static constexpr int P(int s) { return DB == 1 ? s * kStride + 128 : s * kStride; }
@@ -1091,7 +1093,8 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
       auto sums = [&](int o, int slot, uint32_t a_col, uint32_t acc, bool more) {
         const uint64_t b0 = dt + (uint64_t)(slot * (Sh::kStageBytes >> 4) + o * (Sh::kMoveBytes >> 4));
 #pragma unroll
-        for (int k = 0; k < kMove / 16; ++k) mma_ts(acc, a_col + k * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc, more || k ? 1u : 0u, e);
+        for (int k = 0; k < kMove / 16; ++k)
+          mma_ts(acc, a_col + (k >> 1) * Tm::kHalf + (k & 1) * 8, b0 + (uint64_t)(k * (2048 >> 4)), idesc, more || k ? 1u : 0u, e);
       };
       for (int t0 = 0; t0 < n; t0 += 2)
 #pragma unroll
@@ -1182,7 +1185,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
           uint32_t v[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = a[k];
-          tmem_st_x16(tmem + lanes + Tm::P(s) + h * 16, v);
+          tmem_st_x16(tmem + lanes + Tm::P(s) + h * Tm::kHalf, v);
         } else if (partial(t)) {
           // keys that take no part: weight 0 whatever the products left there
           wait_warp(&bar->mready[t % NS], (t / NS) & 1, abort_flag, err);
@@ -1190,7 +1193,7 @@ __device__ __forceinline__ void bwd_pass(const BwdParams& p, int item, uint32_t 
 #pragma unroll
           for (int k = 0; k < 16; ++k) u[k] &= (w >> (2 * k) & 1u ? 0xffffu : 0u) | (w >> (2 * k + 1) & 1u ? 0xffff0000u : 0u);
         }
-        tmem_st_x16(tmem + lanes + Tm::dS(s) + h * 16, u);
+        tmem_st_x16(tmem + lanes + Tm::dS(s) + h * Tm::kHalf, u);
         tmem_st_wait();
       }
       tc_fence_before();

@@ -539,3 +539,16 @@ def test_captured_backward_with_few_rows(sv, q_lens, kv_lens):
         for k, t in zip(("dQ", "dK", "dV"), got):
             assert torch.equal(t, want[k]), (name, k)
     assert sv.svconv_read_error_word() == 0
+
+
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 2, 2), (72, 6, 2)])
+def test_wide_heads_backward_repeats_itself(sv, d, Hq, Hkv):
+    """Above 64 channels the key pass keeps P and dS in the columns of the scores that two threads of a row read at their
+    own pace: no timing may let one thread's results reach the other's scores."""
+    x = make(140 + d, (1500, 700), (900, 1100), Hq, Hkv, d, keep=0.9)
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, f"{d} channels")
+    args = dict(max_q=x["max_q"], max_kv=x["max_kv"], kv_keep=x["keep"])
+    for _ in range(40):
+        again = sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], got["O"], got["lse"], x["q_off"], x["kv_off"], **args)
+        assert all(torch.equal(t, got[k]) for k, t in zip(("dQ", "dK", "dV"), again))
