@@ -365,6 +365,9 @@ struct FwdCursor {
 };
 
 constexpr int kItems = 4;  // items the loader may be ahead
+// Named barriers of the forward kernel: 1 to 8 the two warps of a row quarter (stream x 4 + quarter), 9 to 12 the
+// streams' merge, and the start; 0 is __syncthreads.
+constexpr int kPairBarrier = 1, kMergeBarrier = 9, kStartBarrier = 13;
 
 struct FwdBarriers {
   uint64_t ifull[kItems], iempty[kItems], qfull[2], qempty[2], kvfull[8], kvempty[8], vready[8];
@@ -400,7 +403,7 @@ __device__ __forceinline__ void fwd_output(const FwdParams& p, const FwdItem* it
   using Sh = FwdShape<DB>;
   const int left = min(p.tokens, it->q1 - it->tok0 - (PAIR ? s * p.tokens : 0)) * p.r;
   const bool warp_on = (row & ~31) < left;
-  const int merge_bar = 9 + half * 2 + (row >> 6);  // named barrier of the two streams' warps of two quarters and this half
+  const int merge_bar = kMergeBarrier + half * 2 + (row >> 6);  // named barrier of the two streams' warps of two quarters and this half
   m2 = l > 0.f ? m2 : -INFINITY;  // no key
   if (!(l > 0.f) && !(l == 0.f)) m2 = l;    // NaN scores: carried along
   // split form: the second stream hands its state over, 32 columns of each half at a time
@@ -509,9 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     tmem_relinquish();
   }
   tc_fence_before();
-  // the loader made the barriers itself and needs no tensor memory: it goes ahead
-  if (warp == kLoadWarp) asm volatile("bar.arrive 0, %0;" ::"n"(kThreads) : "memory");
-  else asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
+  // The loader made the barriers itself and needs no tensor memory: it goes ahead.  On a barrier of its own: the loader may
+  // be at the kernel's last __syncthreads before tensor memory is there, and must not be counted twice.
+  if (warp == kLoadWarp) asm volatile("bar.arrive %0, %1;" ::"n"(kStartBarrier), "n"(kThreads) : "memory");
+  else asm volatile("bar.sync %0, %1;" ::"n"(kStartBarrier), "n"(kThreads) : "memory");
   tc_fence_after();
   pdl_wait();
   if (warp != kLoadWarp) pdl_trigger();  // (after the tensor memory: the next kernel's CTAs may come and ask for theirs)
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // ------------------------------------------------------------ softmax: two threads per row, 64 scores each
     const int s = warp >> 3, half = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
     const uint32_t tmem = bar->tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int pair_bar = 1 + s * 4 + (warp & 3);           // named barrier of the two warps that hold the same rows
+    const int pair_bar = kPairBarrier + s * 4 + (warp & 3);           // named barrier of the two warps that hold the same rows
     const float ca = fmaxf(fabsf(p.c), 1e-30f);  // never 0: a masked score stays -inf when scaled
     const uint32_t sb = smem_u32(bar) + s * 8;   // this stream's barriers, at fixed offsets
     int done = 0, seq = 0;                       // steps of this stream and K / V tiles before this item

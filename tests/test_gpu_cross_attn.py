@@ -552,3 +552,17 @@ def test_wide_heads_backward_repeats_itself(sv, d, Hq, Hkv):
     for _ in range(40):
         again = sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], got["O"], got["lse"], x["q_off"], x["kv_off"], **args)
         assert all(torch.equal(t, got[k]) for k, t in zip(("dQ", "dK", "dV"), again))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_items_one_after_the_other(sv, d):
+    """Items of no key tile or one, whose loads are all issued before the rest of the CTA has its tensor memory, in
+    calls that follow each other while the previous one's CTAs still hold theirs."""
+    x = make(150 + d, (1, 3, 2, 5), (0, 7, 128, 90), 2, 1, d)
+    got = run_both(sv, x, backward=False)
+    check(x, got, d ** -0.5, f"short items of {d} channels")
+    args = dict(max_q=x["max_q"], max_kv=x["max_kv"])
+    outs = [sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], **args) for _ in range(300)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(O, got["O"]) and torch.equal(lse, got["lse"]) for O, lse in outs)
+    assert sv.svconv_read_error_word() == 0
