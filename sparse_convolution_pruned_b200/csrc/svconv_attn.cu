@@ -222,7 +222,7 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 __device__ __forceinline__ void store_row(float* dst, const float (&f)[16], int n) {
 #pragma unroll
   for (int k = 0; k < 16; k += 8)
-    if (k < n) st_global_32(dst + k, reinterpret_cast<const uint32_t*>(f) + k);  // rows of 8 k floats: 32-byte aligned
+    if (k < n) st_global_32(dst + k, reinterpret_cast<const uint32_t*>(f) + k);  // rows of 8 k floats from a 32-byte boundary (ws_floats)
 }
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const float (&f)[16], int n, bool wide) {
   uint32_t v[8];
@@ -2033,6 +2033,11 @@ __global__ void __launch_bounds__(256) attn_sum_kernel(const float* part0, const
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// Partial results are stored 32 bytes at a time; a workspace is aligned to 16.  Its first 32-byte boundary, and the
+// bytes that a size has more for it.
+constexpr size_t kWsSlack = 16;
+float* ws_floats(void* p) { return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p) + 31u) & ~(uintptr_t)31u); }
+
 // Rows, and items of a launch: a row, block or item behind the last one still has a 32-bit number.
 constexpr int kMaxRows = 0x7fff0000;
 
@@ -2279,13 +2284,14 @@ size_t svconv_cross_attn_fwd_workspace_size(const svconv_cross_attn_desc* desc) 
   svconv_cross_attn_desc c;
   if (check_desc(desc, c) || c.G == 0 || c.max_q == 0) return 0;
   const FwdPlan f = plan_fwd(c);
-  return f.splits > 1 ? (size_t)f.splits * c.nq * c.Hq * (c.d + 2) * sizeof(float) : 0;
+  return f.splits > 1 ? (size_t)f.splits * c.nq * c.Hq * (c.d + 2) * sizeof(float) + kWsSlack : 0;
 }
 
 size_t svconv_cross_attn_bwd_workspace_size(const svconv_cross_attn_desc* desc) {
   svconv_cross_attn_desc c;
   if (check_desc(desc, c) || c.G == 0) return 0;
-  return plan_bwd(c).floats() * sizeof(float);
+  const size_t floats = plan_bwd(c).floats();
+  return floats ? floats * sizeof(float) + kWsSlack : 0;
 }
 
 int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, const void* K, const void* V, void* O,
@@ -2311,7 +2317,7 @@ int svconv_cross_attn_fwd(const svconv_cross_attn_desc* desc, const void* Q, con
   p.O = static_cast<__nv_bfloat16*>(O);
   p.wide = c.d % 16 == 0 && aligned32(O);
   p.lse = lse;
-  p.part_o = static_cast<float*>(workspace);
+  p.part_o = ws_floats(workspace);
   p.part_ml = p.part_o + (size_t)f.splits * c.nq * c.Hq * c.d;
   p.status = dev_status ? dev_status : device_error_word();
   // no keys at all: the maps only have to be well formed
@@ -2353,7 +2359,7 @@ int svconv_cross_attn_bwd(const svconv_cross_attn_desc* desc, const void* dO, co
   while (lanes < c.d / 8) lanes *= 2;
   const long long stat_grid = (long long)cdiv(c.max_q, kMove / r) * c.Hkv;
   if (q_items + k_items > kMaxRows || stat_grid > kMaxRows) return SVCONV_ERR_SIZE;
-  float* ws = static_cast<float*>(workspace);
+  float* ws = ws_floats(workspace);
   BwdParams p{};
   p.q_off = c.q_off, p.kv_off = c.kv_off, p.keep = c.kv_keep;
   p.nq = c.nq, p.nkv = c.nkv, p.max_q = c.max_q, p.max_kv = c.max_kv, p.Hq = c.Hq, p.Hkv = c.Hkv, p.r = r, p.d = c.d;

@@ -566,3 +566,26 @@ def test_short_items_one_after_the_other(sv, d):
     torch.cuda.synchronize()
     assert all(torch.equal(O, got["O"]) and torch.equal(lse, got["lse"]) for O, lse in outs)
     assert sv.svconv_read_error_word() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens", [((3,), (9000,)), ((3000,), (90,)), ((260,), (20000,)), ((9000,), (260,))])
+def test_workspaces_at_any_16_byte_boundary(sv, q_lens, kv_lens, d):
+    """A caller's workspace of just the bytes asked for, 0 to 48 past a 512-byte boundary, between guards."""
+    x = make(160 + d, q_lens, kv_lens, 2, 2, d)
+    want = run_both(sv, x)
+    _, desc = sv._attn_desc(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], x["max_q"], x["max_kv"], None, None)
+    sizes = sv.svconv_cross_attn_fwd_workspace_size(desc), sv.svconv_cross_attn_bwd_workspace_size(desc)
+    assert max(sizes) > 0
+    args = dict(max_q=x["max_q"], max_kv=x["max_kv"])
+    for at in (0, 16, 32, 48):
+        bufs = [torch.full((at + n + 64,), 0x55, dtype=torch.uint8, device="cuda") for n in sizes]
+        fws, bws = (b[at:at + n] if n else None for b, n in zip(bufs, sizes))
+        O, lse = sv.svconv_cross_attn_fwd(x["Q"], x["K"], x["V"], x["q_off"], x["kv_off"], workspace=fws, **args)
+        grads = sv.svconv_cross_attn_bwd(x["dO"], x["Q"], x["K"], x["V"], O, lse, x["q_off"], x["kv_off"], workspace=bws, **args)
+        torch.cuda.synchronize()
+        for k, t in zip(("O", "lse", "dQ", "dK", "dV"), (O, lse) + grads):
+            assert torch.equal(t, want[k]), (at, k)
+        for b, n in zip(bufs, sizes):
+            assert (b[:at] == 0x55).all() and (b[at + n:] == 0x55).all(), at
+    assert sv.svconv_read_error_word() == 0
