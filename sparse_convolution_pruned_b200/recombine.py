@@ -76,10 +76,11 @@ def recombine_fwd(Q, K, V, pos_q, pos_k, groups: Groups, rotation: Rotation, *, 
 def recombine_bwd(dO, saved: Saved, groups: Groups, rotation: Rotation, *, status=None, stream=None):
     """(dQ, dK, dV bf16, dwq, dwk fp32 [d]) of recombine_fwd.  Rows of no group (a padded batch's) get zero
     gradients; they and left-out keys add nothing to dwq and dwk as long as what they hold is finite."""
-    grads = [torch.empty_like(t, memory_format=torch.contiguous_format) for t in (saved.Yq, saved.Yk, saved.V)]
     with torch.cuda.stream(stream):
+        grads = [torch.zeros_like(t, memory_format=torch.contiguous_format) for t in (saved.Yq, saved.Yk, saved.V)]
+    if stream is not None:  # that stream's memory, which the caller may use on the current one
         for t in grads:
-            t.zero_()
+            t.record_stream(torch.cuda.current_stream(dO.device))
     dYq, dYk, dV = svconv.svconv_cross_attn_bwd(dO, saved.Yq, saved.Yk, saved.V, saved.O, saved.lse, groups.q_off,
                                                 groups.kv_off, max_q=groups.max_q, max_kv=groups.max_kv,
                                                 scale=saved.scale, kv_keep=saved.kv_keep, dQ=grads[0], dK=grads[1],

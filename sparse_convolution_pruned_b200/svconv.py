@@ -427,30 +427,40 @@ def _like(name: str, t: torch.Tensor, shape, dtype, index: int):
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
 
 
-def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int) -> torch.Tensor:
+def _new(shape, dtype, like: torch.Tensor, index: int, stream=None, returned: bool = True) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one) on cuda:index.  On another stream than the current one it is
+    that stream's own memory: what the current stream freed may still be in use there, and what is freed here
+    goes back to the stream that works on it.  The current stream may use what is returned to the caller."""
+    if stream is None or stream.cuda_stream == _stream_now(index):
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
+def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int, stream=None) -> torch.Tensor:
     """An output of like's shape and dtype, contiguous: checked if given, else allocated."""
     if t is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return _new(like.shape, like.dtype, like, index, stream)
     _like(name, t, like.shape, like.dtype, index)
     return t
 
 
-def _f32(name: str, t: Optional[torch.Tensor], shape, like: torch.Tensor, index: int) -> torch.Tensor:
+def _f32(name: str, t: Optional[torch.Tensor], shape, like: torch.Tensor, index: int, stream=None) -> torch.Tensor:
     if t is None:
-        return like.new_empty(shape, dtype=torch.float32)
+        return _new(shape, torch.float32, like, index, stream)
     _like(name, t, shape, torch.float32, index)
     return t
 
 
 def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int, stream=None):
-    """(tensor to keep until the launch, its address, its bytes).  One allocated here, for a call on another
-    stream than the current one, is not given out again before that stream is done with it."""
+    """(tensor to keep until the launch, its address, its bytes)."""
     if ws is None:
         if not need:
             return None, None, 0
-        ws = like.new_empty((need,), dtype=torch.uint8)
-        if stream is not None:
-            ws.record_stream(stream)
+        ws = _new((need,), torch.uint8, like, index, stream, returned=False)
     elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{index} is needed")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -516,8 +526,8 @@ def svconv_cross_attn_fwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, q_o
     scale defaults to 1 / sqrt(d); kv_keep [nkv] (uint8 or bool) leaves keys out.  Rows of no group
     are not written."""
     index, desc = _attn_desc(Q, K, V, q_off, kv_off, max_q, max_kv, scale, kv_keep)
-    out = _same("out", out, Q, index)
-    lse = _f32("lse", lse, Q.shape[:2], Q, index)
+    out = _same("out", out, Q, index, stream)
+    lse = _f32("lse", lse, Q.shape[:2], Q, index, stream)
     L, ref = lib(), ctypes.byref(desc)
     ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_fwd_workspace_size(ref), Q, index, stream)
     _call("svconv_cross_attn_fwd", index, L.svconv_cross_attn_fwd, ref, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
@@ -537,7 +547,7 @@ def svconv_cross_attn_bwd(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V:
     _like("dO", dO, Q.shape, torch.bfloat16, index)
     _like("O", O, Q.shape, torch.bfloat16, index)
     _like("lse", lse, Q.shape[:2], torch.float32, index)
-    dQ, dK, dV = _same("dQ", dQ, Q, index), _same("dK", dK, K, index), _same("dV", dV, V, index)
+    dQ, dK, dV = _same("dQ", dQ, Q, index, stream), _same("dK", dK, K, index, stream), _same("dV", dV, V, index, stream)
     L, ref = lib(), ctypes.byref(desc)
     ws, ws_ptr, ws_bytes = _scratch(workspace, L.svconv_cross_attn_bwd_workspace_size(ref), Q, index, stream)
     _call("svconv_cross_attn_bwd", index, L.svconv_cross_attn_bwd, ref, dO.data_ptr(), Q.data_ptr(), K.data_ptr(),
@@ -595,7 +605,7 @@ def svconv_qk_norm_rope_fwd(Q: torch.Tensor, K: torch.Tensor, pos_q: torch.Tenso
     per unit of position (the first 2 * len(freq) channels are rotated), axis_pairs the number of pairs that
     follow each axis.  Yq / Yk may be Q / K themselves when those are contiguous."""
     index, (sq, sk), args = _qk_common(Q, K, pos_q, pos_k, freq, layout, axis_pairs, wq, wk)
-    Yq, Yk = _same("Yq", Yq, Q, index), _same("Yk", Yk, K, index)
+    Yq, Yk = _same("Yq", Yq, Q, index, stream), _same("Yk", Yk, K, index, stream)
     sq.y, sk.y = Yq.data_ptr(), Yk.data_ptr()
     _call("svconv_qk_norm_rope_fwd", index, lib().svconv_qk_norm_rope_fwd, *args, float(eps), ctypes.byref(sq),
           ctypes.byref(sk), stream.cuda_stream if stream is not None else _stream_now(index))
@@ -618,9 +628,9 @@ def svconv_qk_norm_rope_bwd(dYq: torch.Tensor, dYk: torch.Tensor, Q: torch.Tenso
     d = Q.shape[2]
     _like("dYq", dYq, Q.shape, Q.dtype, index)
     _like("dYk", dYk, K.shape, K.dtype, index)
-    dQ, dK = _same("dQ", dQ, Q, index), _same("dK", dK, K, index)
+    dQ, dK = _same("dQ", dQ, Q, index, stream), _same("dK", dK, K, index, stream)
     if want_dw:
-        dwq, dwk = _f32("dwq", dwq, (d,), Q, index), _f32("dwk", dwk, (d,), Q, index)
+        dwq, dwk = _f32("dwq", dwq, (d,), Q, index, stream), _f32("dwk", dwk, (d,), Q, index, stream)
         sq.dw, sk.dw = dwq.data_ptr(), dwk.data_ptr()
     else:
         dwq = dwk = None
@@ -663,7 +673,7 @@ def svconv_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, out: Op
             raise TypeError(f"fp32 or bf16 gradients are needed, got {set(dtypes)}")
         flat[3::4] = array.array("q", [F32 if t is torch.float32 else BF16 for t in dtypes])
     table = flat.buffer_info()[0] if count else None
-    norm = _f32("norm", norm, (), grads[0] if grads else norm, index)
+    norm = _f32("norm", norm, (), grads[0] if grads else norm, index, stream)
     L = lib()
     ws, ws_ptr, ws_bytes = _scratch(workspace, max(L.svconv_clip_grads_workspace_size(table, count), 16), norm, index, stream)
     _call("svconv_clip_grads", index, L.svconv_clip_grads, table, count, float(max_norm), norm.data_ptr(), ws_ptr, ws_bytes,

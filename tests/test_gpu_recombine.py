@@ -208,3 +208,105 @@ def test_scratch_of_a_call_on_another_stream(sv, monkeypatch):
         assert all(t.data_ptr() != address for t in fresh)
     torch.cuda.synchronize()
     assert sv.svconv_read_error_word() == 0
+
+
+def stream_calls(sv):
+    """Every call that allocates, as call(stream) -> its outputs."""
+    from sparse_convolution_pruned_b200 import recombine as rc
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    off = lambda n: torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    Q, K, V = rnd(40, 2, 64).bfloat16(), rnd(9000, 2, 64).bfloat16(), rnd(9000, 2, 64).bfloat16()
+    pq, pk = (torch.arange(n, dtype=torch.int32, device="cuda") for n in (40, 9000))
+    groups, rot = rc.Groups(off(40), off(9000), 40, 9000), rc.Rotation(rc.axis_frequencies((32,)), (32,))
+    lim, g = dict(max_q=40, max_kv=9000), [rnd(50000), rnd(7).bfloat16()]
+    O, lse = sv.svconv_cross_attn_fwd(Q, K, V, groups.q_off, groups.kv_off, **lim)
+    _, saved = rc.recombine_fwd(Q, K, V, pq, pk, groups, rot)
+    torch.cuda.synchronize()
+    return [
+        lambda s: sv.svconv_cross_attn_fwd(Q, K, V, groups.q_off, groups.kv_off, stream=s, **lim),
+        lambda s: sv.svconv_cross_attn_bwd(Q, Q, K, V, O, lse, groups.q_off, groups.kv_off, stream=s, **lim),
+        lambda s: sv.svconv_qk_norm_rope_fwd(Q, K, pq, pk, rot.freq, stream=s),
+        lambda s: sv.svconv_qk_norm_rope_bwd(Q, K, Q, K, pq, pk, rot.freq, stream=s),
+        lambda s: (sv.svconv_clip_grads(g, math.inf, stream=s),),
+        lambda s: rc.recombine_fwd(Q, K, V, pq, pk, groups, rot, stream=s)[:1],
+        lambda s: rc.recombine_bwd(Q, saved, groups, rot, stream=s),
+    ]
+
+
+def spied(sv, monkeypatch):
+    """The memory that calls allocate, as a list of (address, bytes)."""
+    taken = []
+    new = sv._new
+
+    def spy(*args, **kw):
+        t = new(*args, **kw)
+        taken.append((t.data_ptr(), t.numel() * t.element_size()))
+        return t
+    monkeypatch.setattr(sv, "_new", spy)
+    return taken
+
+
+def overlaps(a, b):
+    return any(x < v + n and v < x + m for x, m in a for v, n in b)
+
+
+def test_dropped_results_of_a_call_on_another_stream(sv, monkeypatch):
+    """What a call on another stream allocated and its caller dropped is not given out on the current stream while the
+    call has yet to write it."""
+    calls, taken, side = stream_calls(sv), spied(sv, monkeypatch), torch.cuda.Stream()
+    for i, call in enumerate(calls):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        del taken[:]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # ~0.1 s
+        got = [(t.data_ptr(), t.numel() * t.element_size()) for t in call(side)]  # dropped at once
+        used = taken + got
+        fresh = [torch.empty((n,), dtype=torch.uint8, device="cuda") for _ in range(4) for _, n in used]
+        assert not overlaps(used, [(t.data_ptr(), t.numel()) for t in fresh]), i
+        del fresh
+    torch.cuda.synchronize()
+    assert sv.svconv_read_error_word() == 0
+
+
+def test_two_calls_at_once_on_two_streams(sv, monkeypatch):
+    """A call on the current stream that has not run yet, and the same call on another stream: no memory in common, and
+    the results of calls one after the other."""
+    calls, side = stream_calls(sv), torch.cuda.Stream()
+    want = [[t.clone() for t in call(None)] for call in calls]
+    taken = spied(sv, monkeypatch)
+    for i, call in enumerate(calls):
+        torch.cuda.synchronize()
+        del taken[:]
+        torch.cuda._sleep(200_000_000)
+        first = call(None)
+        mine = list(taken)
+        del taken[:]
+        second = call(side)
+        assert not overlaps(mine, taken), i
+        assert not overlaps([(t.data_ptr(), t.numel() * t.element_size()) for t in first],
+                            [(t.data_ptr(), t.numel() * t.element_size()) for t in second]), i
+        torch.cuda.synchronize()
+        for got in (first, second):
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i])), i
+    assert sv.svconv_read_error_word() == 0
+
+
+def test_another_stream_under_a_captured_graph(sv):
+    """Calls on a stream that joins the capture of the current one."""
+    calls = stream_calls(sv)
+    want = [[t.clone() for t in call(None)] for call in calls]
+    torch.cuda.synchronize()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        side.wait_stream(main)
+        got = [call(side) for call in calls]
+        main.wait_stream(side)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
