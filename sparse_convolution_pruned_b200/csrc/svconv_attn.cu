@@ -1527,9 +1527,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
           r[(k + j) / 2] = rest_bf16(x, y, u[(k + j) / 2]);
         }
       }
+      // A key that takes no part has weight 0 in dQ; its own gradients are 0 at the store, since 0 times a query's
+      // infinity is not.
+      bool live = true;
       if (partial(t)) {
         wait_warp(&bar->kready[slot], (2 * t / NS) & 1, abort_flag, err);
-        if (!(bar->kept[slot][warp & 3] >> lane & 1u)) {
+        live = bar->kept[slot][warp & 3] >> lane & 1u;
+        if (!live) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) w[k] = u[k] = r[k] = 0u;
         }
@@ -1561,10 +1565,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
         if (key < k1) {
           float v[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) * f;
+          for (int k = 0; k < 16; ++k) v[k] = live ? __uint_as_float(o[k]) * f : 0.f;
           store_row(out + c, v, p.d - c, p.wide);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[16 + k]) * f;
+          for (int k = 0; k < 16; ++k) v[k] = live ? __uint_as_float(o[16 + k]) * f : 0.f;
           store_row(out + c + 16, v, p.d - c - 16, p.wide);
         }
       }
@@ -1926,7 +1930,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __
         const int key = key0 + k;
         if (key >= keys || row >= p.d) continue;
         const int64_t at = ((int64_t)(k0 + key) * p.Hkv + hk) * p.d + row, from = split * ((int64_t)p.nkv * p.Hkv * p.d) + at;
-        const float dv = nt > 0 ? __uint_as_float(o[k]) : 0.f, dk = nt > 0 ? __uint_as_float(w[k]) * p.scale : 0.f;
+        // a key that takes no part: 0 whatever its weights of 0 met in the queries' rows
+        const bool live = nt > 0 && (bar->kept[key >> 5] >> (key & 31) & 1u);
+        const float dv = live ? __uint_as_float(o[k]) : 0.f, dk = live ? __uint_as_float(w[k]) * p.scale : 0.f;
         if (p.ksplits > 1) p.part_v[from] = dv, p.part_k[from] = dk;
         else p.dV[at] = __float2bfloat16(dv), p.dK[at] = __float2bfloat16(dk);
       }

@@ -589,3 +589,28 @@ def test_workspaces_at_any_16_byte_boundary(sv, q_lens, kv_lens, d):
         for b, n in zip(bufs, sizes):
             assert (b[:at] == 0x55).all() and (b[at + n:] == 0x55).all(), at
     assert sv.svconv_read_error_word() == 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,d,Hq", [
+    ((200, 150), (300, 400), 64, 2), ((200, 150), (300, 400), 128, 4),      # two passes
+    ((9, 5), (300, 700), 64, 2), ((3, 8), (20000, 300), 128, 4),            # few queries
+    ((300, 40), (77, 90), 64, 4), ((20000, 700), (50, 64), 128, 2),         # few keys
+])
+def test_dropped_keys_get_zero_gradients_whatever_their_queries_hold(sv, q_lens, kv_lens, d, Hq):
+    """A row of the group's own dO with an infinity, and one of Q with a NaN: a dropped key's gradients are 0 all the
+    same, and rows and groups that do not meet those values keep theirs."""
+    x = make(170 + d + Hq, q_lens, kv_lens, Hq, 2, d, keep=0.6)
+    clean = run_both(sv, x)
+    x["dO"][1, 0, 3] = math.inf
+    x["Q"][2, Hq - 1, 5] = math.nan
+    got = run_both(sv, x)
+    drop = x["keep"] == 0
+    assert drop.any()
+    assert (got["dK"][drop] == 0).all() and (got["dV"][drop] == 0).all()
+    rows = torch.ones(sum(q_lens), dtype=torch.bool, device="cuda")
+    rows[1:3] = False
+    for k in ("O", "lse", "dQ"):
+        assert torch.equal(got[k][rows], clean[k][rows]), k
+    for k in ("dK", "dV"):
+        assert torch.equal(got[k][kv_lens[0]:], clean[k][kv_lens[0]:]), k
+        assert not torch.isfinite(got[k][:kv_lens[0]][~drop[:kv_lens[0]]]).all()
