@@ -293,7 +293,8 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *     P = softmax_j(S),   O[i][h] = sum_j P[i][j] V[j][h / r],   lse[i][h] = log sum_j exp(S[i][j])
  * A row whose group has no kept key gets O = 0 and lse = -inf.  The scores, the softmax's
  * statistics and all sums are fp32; P (and dS below) are rounded to bf16 as matrix operands (dS to
- * two bf16 values where a group has at most 64 keys or 32 query rows, tokens x heads of a key head).
+ * two bf16 values where the bounds say that every group has at most 64 keys or at most 32 query rows: max_kv <= 64 or
+ * max_q * (Hq / Hkv) <= 32; from 65 to 96 keys under more query rows it is one).
  *   Q [nq][Hq][d], K and V [nkv][Hkv][d] bf16 with the given row and head strides (in
  *   elements, multiples of 8; channels contiguous), 16-byte aligned; O [nq][Hq][d] bf16 and
  *   lse [nq][Hq] fp32, contiguous.  kv_keep [nkv] or NULL: keys with a zero byte are left out,
@@ -312,7 +313,8 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *
  * svconv_cross_attn_bwd: with dO [nq][Hq][d] bf16 and O, lse of the forward call,
  *     dP = dO V^T,  D[i] = dO[i] . O[i],  dS = P * (dP - D),
- *   (where max_kv <= 96, D[i] = sum_j P[i][j] dP[i][j], the same without O's rounding)
+ *   (where max_kv <= 64, or max_kv <= 96 and max_q * (Hq / Hkv) > 32, D[i] = sum_j P[i][j] dP[i][j], the same
+ *   without O's rounding, and O is not read)
  *     dQ = scale dS K,  dK = scale sum over the r query heads of dS^T Q,  dV = the same of P^T dO
  *   into dQ [nq][Hq][d], dK and dV [nkv][Hkv][d] bf16 (contiguous, overwritten; rows of dropped
  *   keys get 0).  Overlapping outputs are not allowed.  No atomics: deterministic.

@@ -1630,6 +1630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
 // whose A operands are the query tiles read MN-major.  Four threads share a query row, so that few registers hold a tile;
 // two groups of warps on alternate tiles gained 4% at 64 channels and lost 15% at 128, where P and dS have one place.
 constexpr int kFewKeys = 96;
+constexpr int kTwoKeys = 64;  // up to so many dS is two bf16 values
 constexpr int kFewKeyBlock = kFewKeys * 128;  // bytes of a 64-channel block of the keys
 
 struct FewKeyBarriers {
@@ -1650,7 +1651,7 @@ struct FewKeyShape {
   static constexpr int kTmS = 0, kTmdP = 96, kTmdQ = 192, kTmdV = 320, kTmdK = 416;
 };
 
-template <int DB, bool TWO>  // TWO: at most 64 keys, dS in two values
+template <int DB, bool TWO>  // TWO: at most kTwoKeys keys, dS in two values
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_keys_kernel(const __grid_constant__ BwdParams p) {
   using Sh = FewKeyShape<DB>;
   constexpr int NS = Sh::kStages;
@@ -2223,7 +2224,12 @@ BwdPlan plan_bwd(const svconv_cross_attn_desc& c) {
                        (sq > 1 ? kBwdMerge + bq * sq : 0.0) + (sk > 1 ? kBwdMerge + bk * sk : 0.0);
       if (best == 0.0 || t < best) best = t, b.qsplits = sq, b.ksplits = sk, b.keys_first = kf;
     }
-  b.few = c.max_q == 0 || c.max_kv == 0 ? 0 : c.max_kv <= kFewKeys ? 2 : (int64_t)c.max_q * r <= kFew ? 1 : 0;
+  // The forms for few rows, by the bounds.  Where both would do, the one that gives dS two bf16 values: few keys up to
+  // kTwoKeys of them, few queries above (also the faster there: 64 x 8 queries over 96 keys, 8 heads of 128, 31 us and 47).
+  if (c.max_q == 0 || c.max_kv == 0) b.few = 0;
+  else if (c.max_kv <= kTwoKeys) b.few = 2;
+  else if ((int64_t)c.max_q * r <= kFew) b.few = 1;
+  else b.few = c.max_kv <= kFewKeys ? 2 : 0;
   if (b.few) {  // one item a split of a group's keys (queries) and key head
     const int tiles = b.few == 1 ? cdiv(c.max_kv, kTile) : cdiv(c.max_q, kTile / r);
     const double units = (double)G * c.Hkv, tile = (b.few == 1 ? kFewTile : kFewKeyTile) * (c.d <= 64 ? 1 : 2);
@@ -2262,7 +2268,7 @@ cudaError_t launch_few(const BwdParams& p, int grid, cudaStream_t s) {
 template <int DB>
 cudaError_t launch_few_keys(const BwdParams& p, int grid, cudaStream_t s) {
   static int done[2][64];
-  const bool two = p.max_kv <= 64;
+  const bool two = p.max_kv <= kTwoKeys;
   auto kernel = two ? attn_bwd_few_keys_kernel<DB, true> : attn_bwd_few_keys_kernel<DB, false>;
   cudaError_t e = ensure_smem_attr(kernel, FewKeyShape<DB>::kSmem, done[two]);
   return e == cudaSuccess ? launch_pdl(kernel, dim3(grid), dim3(kThreads), FewKeyShape<DB>::kSmem, s, p) : e;

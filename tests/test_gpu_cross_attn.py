@@ -614,3 +614,17 @@ def test_dropped_keys_get_zero_gradients_whatever_their_queries_hold(sv, q_lens,
     for k in ("dK", "dV"):
         assert torch.equal(got[k][kv_lens[0]:], clean[k][kv_lens[0]:]), k
         assert not torch.isfinite(got[k][:kv_lens[0]][~drop[:kv_lens[0]]]).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,d", [((13,), (77,), 4, 4, 80), ((13,), (96,), 4, 4, 80), ((8, 3), (70, 65), 2, 2, 128),
+                                                     ((4, 2, 1), (90, 66, 80), 8, 1, 64)])
+def test_few_queries_over_65_to_96_keys(sv, q_lens, kv_lens, Hq, Hkv, d):
+    """At most 32 query rows: dS in 16 bits of significand there too, as over fewer or more keys (the bound of the test of
+    norms above)."""
+    x = make(180 + d, q_lens, kv_lens, Hq, Hkv, d)
+    got = run_both(sv, x)
+    check(x, got, d ** -0.5, "few by few")
+    ref, _ = reference(x, d ** -0.5)
+    for k in ("dQ", "dK"):
+        off = float((got[k].double() - ref[k]).norm() / ref[k].norm())
+        assert off <= 1.05 * U / math.sqrt(3), (k, off)
