@@ -351,7 +351,8 @@ SVCONV_API size_t svconv_cross_attn_bwd_workspace_size(const svconv_cross_attn_d
  *   axis_pairs[1] axis 1, and so on (host array of `axes` counts that add up to rot / 2), so
  *   the coords table of svconv_build_index, (t, y, x) per token, serves as pos with axes = 3.
  *   freq is fp64 [rot / 2] DEVICE, radians per unit of position: any spacing or scaling for
- *   long sequences is the caller's.  Angles are formed in fp64, so far positions lose nothing.
+ *   long sequences is the caller's.  Angles are formed modulo one turn in integers, off by at
+ *   most 2^-32 turns + 2^-64 turns per unit of position: far positions lose nothing in fp32.
  *   A side with n = 0 is skipped (its pointers may be NULL).
  *   x [n][H][d] of dtype (SVCONV_F32 or SVCONV_BF16) with a row stride in elements (a multiple
  *   of 8, heads contiguous); y, dy, dx [n][H][d] contiguous; pos int32 [n][axes]; w fp32 [d] or

@@ -8,10 +8,12 @@
 // of its four pairs, so a norm is a few shuffles and a rotation none.  Four chunks per lane are in
 // flight before the trigonometry starts.
 //
-// Angles: a pair's frequency in turns per position is kept as a 64-bit binary fraction; its product with the
-// position, modulo one turn, is three integer operations and off by less than 2^-33 turns at any position.
-// All other arithmetic is fp32 and rounds once, at the store.  The bf16 forms take sin.approx /
-// cos.approx (error below 2^-20.9 on one turn, 2^-12 of a bf16 rounding), the fp32 forms sincospif.
+// Angles: a pair's frequency in turns per position, formed in two doubles, is kept as a 64-bit binary fraction (off by
+// 2^-64); its product with the position, modulo one turn and rounded to 32 bits, is three integer operations and off by
+// less than 2^-32 turns + 2^-64 turns a position, 2^-31 at the farthest.  The fp32 forms take the quarter turn off as an
+// integer, so that 24 bits hold the rest (2^-27 of half a turn), and sincospif; the bf16 forms round the
+// whole fraction to 24 bits and take sin.approx / cos.approx (error below 2^-20.9 on one turn, 2^-12 of a bf16 rounding).
+// All other arithmetic is fp32 and rounds once, at the store.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -29,6 +31,8 @@ constexpr int kQkCtas = 4 * kQkSms;
 constexpr int kQkMaxD = 256;
 constexpr int kQkBatch = 4;     // chunks (8 channels a lane) in flight
 constexpr int kQkMaxPairs = kQkMaxD / 2;
+constexpr double kTwo64 = 18446744073709551616.0;
+constexpr double kInvTwoPi = 0.15915494309189535, kInvTwoPiRest = -9.839338337591243e-18;  // 1 / (2 pi) in two doubles
 
 struct QkSide {
   const void *x, *dy;
@@ -185,9 +189,16 @@ __device__ __forceinline__ void rotate(Pairs& v, const float* cs, const float* s
 template <typename T>
 __device__ __forceinline__ void turn_by(unsigned long long f, int pos, float& s, float& c) {
   const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32);
-  const uint32_t frac = hi * (uint32_t)pos + __umulhi(lo, (uint32_t)pos) - (pos < 0 ? lo : 0u);
+  const uint32_t low = (uint32_t)(((unsigned long long)lo * (uint32_t)pos + 0x80000000ull) >> 32);  // rounded
+  const uint32_t frac = hi * (uint32_t)pos + low - (pos < 0 ? lo : 0u);
   if constexpr (sizeof(T) == 4) {
-    sincospif((float)(int)frac * 4.656612873077393e-10f, &s, &c);  // 2^-31: the angle over pi, -1 .. 1
+    const uint32_t q = frac + 0x20000000u;  // the nearest quarter turn in the top two bits
+    float sr, cr;
+    sincospif((float)(int)(frac - (q & 0xc0000000u)) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31: over pi, -1/4 .. 1/4
+    s = q & 0x40000000u ? cr : sr;
+    c = q & 0x40000000u ? sr : cr;
+    if (q & 0x80000000u) s = -s;
+    if ((q + 0x40000000u) & 0x80000000u) c = -c;
   } else {
     const float x = (float)(int)frac * 1.4629180792671596e-9f;  // 2 pi 2^-32
     s = __sinf(x);
@@ -325,8 +336,9 @@ __global__ void __launch_bounds__(kQkWarps * 32, kQkPerSm<T, BWD>) qk_kernel(con
   pdl_wait();
   pdl_trigger();
   if ((int)threadIdx.x < p.pairs) {
-    const double t = p.freq[threadIdx.x] * 0.15915494309189533577;
-    s_turn[threadIdx.x] = (unsigned long long)__double2ll_rn((t - rint(t)) * 18446744073709551616.0);
+    // freq / (2 pi) as t + rest: the product's rounding error, and the part of 1 / (2 pi) that one double leaves out
+    const double f = p.freq[threadIdx.x], t = f * kInvTwoPi, rest = fma(f, kInvTwoPi, -t) + f * kInvTwoPiRest;
+    s_turn[threadIdx.x] = (unsigned long long)__double2ll_rn((t - rint(t)) * kTwo64) + (unsigned long long)__double2ll_rn(rest * kTwo64);
   }
   __syncthreads();
   const bool is_k = (int)blockIdx.x >= p.side[0].ctas;

@@ -170,3 +170,44 @@ def test_captured_graph(sv):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("lo,hi", [(0, 282624), (2 ** 30, 2 ** 31 - 1)])
+def test_fp32_angles_at_any_position(sv, layout, lo, hi):
+    """(2, 0) turned by the angle, against the angle as a rational number of turns.  The norm of these rows is exactly 1,
+    so the turned pair is off by the sine and cosine alone: one unit in the last place each (2^-24), an angle held in
+    24 bits on an eighth of a turn either way (2^-27 of half a turn) and the turn's fraction in 32 bits.  In the mean
+    square a rounding is 1 / sqrt(3) of its bound."""
+    n, pairs, d = 500, 16, 32
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(lo % 1000)
+    pos = torch.randint(lo, hi, (n,), generator=gen, device="cuda").int()
+    pos[0], pos[1::2] = 0, -pos[1::2]
+    x = torch.zeros((n, 1, d), device="cuda")
+    a, b = (torch.arange(8), torch.arange(8) + pairs) if layout == "half" else (2 * torch.arange(8), 2 * torch.arange(8) + 1)
+    x[..., a] = 2.0
+    freq = (10000.0 ** (-torch.arange(pairs, dtype=torch.float64) / pairs)).cuda()
+    empty = x[:0], pos[:0]
+    y, _ = sv.svconv_qk_norm_rope_fwd(x, empty[0], pos, empty[1], freq, eps=0.0, layout=layout)
+    assert (y[0, 0, a] == 2).all() and (y[0, 0, b] == 0).all()
+    # turns = pos * freq / (2 pi) modulo 1, 1 / (2 pi) from pi = 16 atan(1/5) - 4 atan(1/239) in integers
+    bits = 256
+    def atan_inv(m):
+        s, term, k = 0, (1 << bits) // m, 1
+        while term:
+            s += term // k if k % 4 == 1 else -(term // k)
+            term, k = term // (m * m), k + 2
+        return s
+    two_pi = 2 * (16 * atan_inv(5) - 4 * atan_inv(239))
+    off = []
+    for i in range(8):
+        num, den = float(freq[i]).as_integer_ratio()
+        for p, ya, yb in zip(pos.tolist(), y[:, 0, a[i]].tolist(), y[:, 0, b[i]].tolist()):
+            turns = (p * num << bits + 64) // (den * two_pi)  # units of 2^-64
+            part = ((turns + (1 << 63)) % (1 << 64) - (1 << 63)) / 2.0 ** 64
+            ang = 2 * math.pi * part
+            off.append((yb * math.cos(ang) - ya * math.sin(ang)) / 2)
+    rms = math.sqrt(sum(v * v for v in off) / len(off))
+    bound = math.sqrt((2.0 ** -24) ** 2 + (math.pi * 2.0 ** -27) ** 2 + (2 * math.pi * 2.0 ** -32) ** 2) / math.sqrt(3)
+    assert rms <= bound, (rms, bound)
