@@ -518,7 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
   else asm volatile("bar.sync %0, %1;" ::"n"(kStartBarrier), "n"(kThreads) : "memory");
   tc_fence_after();
   pdl_wait();
-  if (warp != kLoadWarp) pdl_trigger();  // (after the tensor memory: the next kernel's CTAs may come and ask for theirs)
+  // After the tensor memory is there: the next kernel's CTAs may come and ask for theirs.  So not from the loader, which does
+  // not wait for it.
+  if (warp != kLoadWarp) pdl_trigger();
 
   int loaded = 0, qloaded = 0;  // K / V tiles and query sets whose loads were issued
   if (warp == kLoadWarp) {
@@ -565,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         if (f) atomicOr(err, f);
       }
     }
-    pdl_trigger();
   } else if (warp == kScoreWarp) {
     const uint32_t e = lane == 0;
     const int ks = (p.d + 15) / 16;

@@ -310,3 +310,27 @@ def test_another_stream_under_a_captured_graph(sv):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_attention_and_convolutions_in_turn(sv, d):
+    """Kernels that follow each other closely and all use tensor memory: the results of calls with waits between them."""
+    w = wl.custom_conv(seed=6, T=6, H=16, W=16, keep_frac=0.3, Cin=64, Cout=64, dtype="bf16")
+    dev = lambda a, dt=None: torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda() if dt else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    X, Wt, coords, foff = dev(w.X, torch.bfloat16), dev(w.Wt, torch.bfloat16), dev(w.coords), dev(w.frame_off)
+    nbr, _ = sv.svconv_build_index(coords, foff, w.T, w.H, w.W)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    off = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    Q, K, V = rnd(200, 2, d).bfloat16(), rnd(300, 2, d).bfloat16(), rnd(300, 2, d).bfloat16()
+    qo, ko = off(0, 2, 2, 200), off(0, 1, 120, 300)
+    step = lambda: (sv.svconv_fwd(X, nbr, Wt), *sv.svconv_cross_attn_fwd(Q, K, V, qo, ko, max_q=198, max_kv=180))
+    want = []
+    for t in step():
+        torch.cuda.synchronize()
+        want.append(t.clone())
+    got = [step() for _ in range(200)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    assert sv.svconv_read_error_word() == 0
