@@ -8,6 +8,9 @@ raises.
 Function names match the C entry points.  Output tensors may be passed in
 (``out=``-style keyword arguments); otherwise they are allocated with torch on
 the input's device.
+
+``stream`` is the torch stream to launch on (default: the current one).  Ordering it with the streams that
+write the inputs and read the outputs is the caller's part; what a call allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -181,6 +184,25 @@ def _cuda(*ts):
             raise ValueError("svconv expects contiguous tensors")
 
 
+# The current device and raw stream without the Python objects around them, where this torch offers them.
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _new(shape, dtype, like: torch.Tensor, index: int, stream=None, returned: bool = True) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one) on cuda:index.  On another stream than the current one it is
+    that stream's own memory: what the current stream freed may still be in use there, and what is freed here
+    goes back to the stream that works on it.  The current stream may use what is returned to the caller."""
+    if stream is None or stream.cuda_stream == _stream_now(index):
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(index))
+    return t
+
+
 def svconv_build_index(coords: torch.Tensor, frame_off: torch.Tensor, T: int, H: int, W: int, *,
                        nbr: Optional[torch.Tensor] = None, M: Optional[torch.Tensor] = None,
                        want_map: bool = False, status: Optional[torch.Tensor] = None,
@@ -188,11 +210,10 @@ def svconv_build_index(coords: torch.Tensor, frame_off: torch.Tensor, T: int, H:
     """Neighbour table [n, 9] int32 (and the lookup map [T, H, W] if requested)."""
     _cuda(coords, frame_off, nbr, M, status)
     n = coords.shape[0]
-    dev = coords.device
     if nbr is None:
-        nbr = torch.empty((n, 9), dtype=torch.int32, device=dev)
+        nbr = _new((n, 9), torch.int32, coords, coords.get_device(), stream)
     if M is None and want_map:
-        M = torch.empty((T, H, W), dtype=torch.int32, device=dev)
+        M = _new((T, H, W), torch.int32, coords, coords.get_device(), stream)
     rc = lib().svconv_build_index(_ptr(coords), _ptr(frame_off), int(T), int(H), int(W), int(n), _ptr(nbr),
                                   _ptr(M), _ptr(status), _stream(coords, stream))
     _check("svconv_build_index", rc)
@@ -207,7 +228,7 @@ def svconv_fwd(X: torch.Tensor, nbr: torch.Tensor, Wt: torch.Tensor, bias: Optio
     Cout = Wt.shape[0]
     if Y is None:
         ydt = torch.bfloat16 if X.dtype == torch.float8_e4m3fn else X.dtype
-        Y = torch.empty((n, Cout), dtype=ydt, device=X.device)
+        Y = _new((n, Cout), ydt, X, X.get_device(), stream)
     rc = lib().svconv_fwd(_dtype_code(X), _ptr(X), _ptr(nbr), n, Cin, Cout, _ptr(Wt), _ptr(bias), _ptr(Y),
                           _stream(X, stream))
     _check("svconv_fwd", rc)
@@ -221,7 +242,7 @@ def svconv_bwd_data(dY: torch.Tensor, nbr: torch.Tensor, Wt: torch.Tensor, *, dX
     n, Cout = dY.shape
     Cin = Wt.shape[2]
     if dX is None:
-        dX = torch.empty((n, Cin), dtype=dY.dtype, device=dY.device)
+        dX = _new((n, Cin), dY.dtype, dY, dY.get_device(), stream)
     rc = lib().svconv_bwd_data(_dtype_code(dY), _ptr(dY), _ptr(nbr), n, Cin, Cout, _ptr(Wt), _ptr(dX),
                                _stream(dY, stream))
     _check("svconv_bwd_data", rc)
@@ -241,12 +262,12 @@ def svconv_bwd_weight(dY: torch.Tensor, X: torch.Tensor, nbr: torch.Tensor, *, d
     Cin = X.shape[1]
     dt = _dtype_code(X)
     if dW is None:
-        dW = torch.empty((Cout, 9, Cin), dtype=torch.float32, device=X.device)
+        dW = _new((Cout, 9, Cin), torch.float32, X, X.get_device(), stream)
     if db is None and want_db:
-        db = torch.empty((Cout,), dtype=torch.float32, device=X.device)
+        db = _new((Cout,), torch.float32, X, X.get_device(), stream)
     need = svconv_bwd_weight_workspace_size(dt, n, Cin, Cout)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=X.device)
+        workspace = _new((max(need, 16),), torch.uint8, X, X.get_device(), stream, returned=False)
     rc = lib().svconv_bwd_weight(dt, _ptr(dY), _ptr(X), _ptr(nbr), n, Cin, Cout, _ptr(dW), _ptr(db),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
                                  _stream(X, stream))
@@ -263,9 +284,9 @@ def svconv_bwd_weight_noalloc(dY: torch.Tensor, X: torch.Tensor, nbr: torch.Tens
     n, Cout = dY.shape
     Cin = X.shape[1]
     if dW is None:
-        dW = torch.empty((Cout, 9, Cin), dtype=torch.float32, device=X.device)
+        dW = _new((Cout, 9, Cin), torch.float32, X, X.get_device(), stream)
     if db is None and want_db:
-        db = torch.empty((Cout,), dtype=torch.float32, device=X.device)
+        db = _new((Cout,), torch.float32, X, X.get_device(), stream)
     rc = lib().svconv_bwd_weight_noalloc(_dtype_code(X), _ptr(dY), _ptr(X), _ptr(nbr), n, Cin, Cout, _ptr(dW),
                                          _ptr(db), _stream(X, stream))
     _check("svconv_bwd_weight_noalloc", rc)
@@ -285,14 +306,14 @@ def svconv_bwd(dY: torch.Tensor, X: torch.Tensor, nbr: torch.Tensor, Wt: torch.T
     Cin = X.shape[1]
     dt = _dtype_code(X)
     if dX is None:
-        dX = torch.empty((n, Cin), dtype=dY.dtype, device=dY.device)
+        dX = _new((n, Cin), dY.dtype, dY, dY.get_device(), stream)
     if dW is None:
-        dW = torch.empty((Cout, 9, Cin), dtype=torch.float32, device=X.device)
+        dW = _new((Cout, 9, Cin), torch.float32, X, X.get_device(), stream)
     if db is None and want_db:
-        db = torch.empty((Cout,), dtype=torch.float32, device=X.device)
+        db = _new((Cout,), torch.float32, X, X.get_device(), stream)
     need = svconv_bwd_workspace_size(dt, n, Cin, Cout)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=X.device)
+        workspace = _new((max(need, 16),), torch.uint8, X, X.get_device(), stream, returned=False)
     rc = lib().svconv_bwd(dt, _ptr(dY), _ptr(X), _ptr(nbr), n, Cin, Cout, _ptr(Wt), _ptr(dX), _ptr(dW), _ptr(db),
                           _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(X, stream))
     _check("svconv_bwd", rc)
@@ -307,14 +328,14 @@ def svconv_bwd_single_pass(dY: torch.Tensor, X: torch.Tensor, nbr: torch.Tensor,
     _cuda(dY, X, nbr, Wt, dX, dW, db, workspace)
     n = dY.shape[0]
     if dX is None:
-        dX = torch.empty((n, 64), dtype=dY.dtype, device=dY.device)
+        dX = _new((n, 64), dY.dtype, dY, dY.get_device(), stream)
     if dW is None:
-        dW = torch.empty((64, 9, 64), dtype=torch.float32, device=X.device)
+        dW = _new((64, 9, 64), torch.float32, X, X.get_device(), stream)
     if db is None and want_db:
-        db = torch.empty((64,), dtype=torch.float32, device=X.device)
+        db = _new((64,), torch.float32, X, X.get_device(), stream)
     need = int(lib().svconv_bwd_single_pass_workspace_size(int(n)))
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=X.device)
+        workspace = _new((max(need, 16),), torch.uint8, X, X.get_device(), stream, returned=False)
     rc = lib().svconv_bwd_single_pass(_ptr(dY), _ptr(X), _ptr(nbr), n, _ptr(Wt), _ptr(dX), _ptr(dW), _ptr(db),
                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
                                       _stream(X, stream))
@@ -336,7 +357,7 @@ def svconv_adapter_fwd(X: torch.Tensor, nbr: torch.Tensor, frame_off: torch.Tens
     R = Wd.shape[0]
     need = svconv_adapter_workspace_size(R, max_chunk_rows)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=X.device)
+        workspace = _new((max(need, 16),), torch.uint8, X, X.get_device(), stream, returned=False)
     rc = lib().svconv_adapter_fwd(_ptr(X), _ptr(nbr), _ptr(frame_off), int(T), n, D, R, _ptr(Wd), _ptr(Wc),
                                   _ptr(bc), _ptr(Wu), int(chunk_T), int(max_chunk_rows), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _ptr(status), _stream(X, stream))
@@ -356,10 +377,10 @@ def svconv_xattn_aux(H: torch.Tensor, group_off: torch.Tensor, aux: torch.Tensor
     n, R = H.shape
     G, A, _ = aux.shape
     if out is None:
-        out = torch.empty((G, A, R), dtype=torch.float32, device=aux.device)
+        out = _new((G, A, R), torch.float32, aux, aux.get_device(), stream)
     need = svconv_xattn_workspace_size(G, max_group_rows, A)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=aux.device)
+        workspace = _new((max(need, 16),), torch.uint8, aux, aux.get_device(), stream, returned=False)
     rc = lib().svconv_xattn_aux(_ptr(H), n, R, _ptr(group_off), G, int(max_group_rows), _ptr(aux), A, int(heads),
                                 _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                 _ptr(status), _stream(aux, stream))
@@ -383,10 +404,10 @@ def svconv_adapter_fwd_xattn(X: torch.Tensor, nbr: torch.Tensor, frame_off: torc
     R = Wd.shape[0]
     A = aux.shape[0]
     if aux_out is None:
-        aux_out = torch.empty((A, R), dtype=torch.float32, device=X.device)
+        aux_out = _new((A, R), torch.float32, X, X.get_device(), stream)
     need = svconv_adapter_xattn_workspace_size(T, R, chunk_T, max_chunk_rows, A)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=X.device)
+        workspace = _new((max(need, 16),), torch.uint8, X, X.get_device(), stream, returned=False)
     rc = lib().svconv_adapter_fwd_xattn(_ptr(X), _ptr(nbr), _ptr(frame_off), int(T), n, D, R, _ptr(Wd), _ptr(Wc),
                                         _ptr(bc), _ptr(Wu), int(chunk_T), int(max_chunk_rows), _ptr(aux), A,
                                         int(heads), _ptr(aux_out), _ptr(workspace),
@@ -401,12 +422,6 @@ def _device_of(t: torch.Tensor) -> int:
     if index < 0:
         raise ValueError("svconv operates on CUDA tensors only")
     return index
-
-
-# The current device and raw stream without the Python objects around them, where this torch offers them.
-_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_stream_now = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(name: str, index: int, fn, *args):
@@ -425,19 +440,6 @@ def _like(name: str, t: torch.Tensor, shape, dtype, index: int):
     if t.get_device() != index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {tuple(shape)} {dtype} on cuda:{index} is needed, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}, strides {t.stride()}")
-
-
-def _new(shape, dtype, like: torch.Tensor, index: int, stream=None, returned: bool = True) -> torch.Tensor:
-    """Memory for a call on `stream` (None: the current one) on cuda:index.  On another stream than the current one it is
-    that stream's own memory: what the current stream freed may still be in use there, and what is freed here
-    goes back to the stream that works on it.  The current stream may use what is returned to the caller."""
-    if stream is None or stream.cuda_stream == _stream_now(index):
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(index))
-    return t
 
 
 def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int, stream=None) -> torch.Tensor:

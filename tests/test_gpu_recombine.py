@@ -334,3 +334,56 @@ def test_short_attention_and_convolutions_in_turn(sv, d):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
     assert sv.svconv_read_error_word() == 0
+
+
+def test_convolution_calls_on_another_stream(sv, monkeypatch):
+    """The two tests above for the convolution, the adapter and the attention of auxiliary tokens."""
+    w = wl.custom_conv(seed=8, T=8, H=16, W=16, keep_frac=0.4, Cin=64, Cout=64, dtype="bf16")
+    dev = lambda a, dt=None: torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda() if dt else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    X, Wt, dY = (dev(a, torch.bfloat16) for a in (w.X, w.Wt, w.dY))
+    coords, foff = dev(w.coords), dev(w.frame_off)
+    nbr, _ = sv.svconv_build_index(coords, foff, w.T, w.H, w.W)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(9)
+    rnd = lambda *s: (0.1 * torch.randn(s, generator=gen, device="cuda")).bfloat16()
+    rows = int(np.diff(w.frame_off).max()) * 4
+    H, Wd, Wc, Wu, aux = rnd(w.n, 128), rnd(64, 128), rnd(64, 9, 64), rnd(128, 64), rnd(1, 4, 64)
+    goff = torch.tensor([0, w.n], dtype=torch.int32, device="cuda")
+    calls = [
+        lambda s: sv.svconv_build_index(coords, foff, w.T, w.H, w.W, want_map=True, stream=s),
+        lambda s: (sv.svconv_fwd(X, nbr, Wt, stream=s), sv.svconv_bwd_data(dY, nbr, Wt, stream=s)),
+        lambda s: sv.svconv_bwd_weight(dY, X, nbr, stream=s),
+        lambda s: sv.svconv_bwd(dY, X, nbr, Wt, stream=s),
+        lambda s: sv.svconv_bwd_single_pass(dY, X, nbr, Wt, stream=s),
+        lambda s: (sv.svconv_xattn_aux(X, goff, aux, max_group_rows=w.n, stream=s),),
+    ]
+    adapter = lambda Y, s: sv.svconv_adapter_fwd_xattn(Y, nbr, foff, w.T, Wd, Wc, Wu, aux[0], chunk_T=4, max_chunk_rows=rows, stream=s)
+    want = [[t.clone() for t in call(None)] for call in calls] + [[t.clone() for t in adapter(H.clone(), None)]]
+    torch.cuda.synchronize()
+    taken, side = spied(sv, monkeypatch), torch.cuda.Stream()
+    for i in range(len(want)):
+        call = calls[i] if i < len(calls) else lambda s: adapter(H.clone() if s is None else Y, s)
+        Y = H.clone()
+        torch.cuda.synchronize()
+        del taken[:]
+        torch.cuda._sleep(200_000_000)
+        first, mine = call(None), list(taken)
+        del taken[:]
+        second = call(side)
+        assert taken and not overlaps(mine, taken), i
+        torch.cuda.synchronize()
+        for got in (first, second):
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i])), i
+        first = second = got = None
+        Y = H.clone()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        del taken[:]
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        call(side)  # dropped at once
+        fresh = [torch.empty((n,), dtype=torch.uint8, device="cuda") for _ in range(4) for _, n in taken]
+        assert not overlaps(taken, [(t.data_ptr(), t.numel()) for t in fresh]), i
+        del fresh
+    torch.cuda.synchronize()
+    assert sv.svconv_read_error_word() == 0
