@@ -445,6 +445,8 @@ def _like(name: str, t: torch.Tensor, shape, dtype, index: int):
 def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int, stream=None) -> torch.Tensor:
     """An output of like's shape and dtype, contiguous: checked if given, else allocated."""
     if t is None:
+        if stream is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
         return _new(like.shape, like.dtype, like, index, stream)
     _like(name, t, like.shape, like.dtype, index)
     return t
@@ -452,7 +454,7 @@ def _same(name: str, t: Optional[torch.Tensor], like: torch.Tensor, index: int, 
 
 def _f32(name: str, t: Optional[torch.Tensor], shape, like: torch.Tensor, index: int, stream=None) -> torch.Tensor:
     if t is None:
-        return _new(shape, torch.float32, like, index, stream)
+        return like.new_empty(shape, dtype=torch.float32) if stream is None else _new(shape, torch.float32, like, index, stream)
     _like(name, t, shape, torch.float32, index)
     return t
 
@@ -462,7 +464,10 @@ def _scratch(ws: Optional[torch.Tensor], need: int, like: torch.Tensor, index: i
     if ws is None:
         if not need:
             return None, None, 0
-        ws = _new((need,), torch.uint8, like, index, stream, returned=False)
+        if stream is None:
+            ws = like.new_empty((need,), dtype=torch.uint8)
+        else:
+            ws = _new((need,), torch.uint8, like, index, stream, returned=False)
     elif ws.get_device() != index or not ws.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{index} is needed")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()

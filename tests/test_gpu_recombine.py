@@ -281,11 +281,11 @@ def test_two_calls_at_once_on_two_streams(sv, monkeypatch):
         torch.cuda.synchronize()
         del taken[:]
         torch.cuda._sleep(200_000_000)
-        first = call(None)
+        first = call(torch.cuda.current_stream())
         mine = list(taken)
         del taken[:]
         second = call(side)
-        assert not overlaps(mine, taken), i
+        assert mine and not overlaps(mine, taken), i
         assert not overlaps([(t.data_ptr(), t.numel() * t.element_size()) for t in first],
                             [(t.data_ptr(), t.numel() * t.element_size()) for t in second]), i
         torch.cuda.synchronize()
@@ -362,12 +362,12 @@ def test_convolution_calls_on_another_stream(sv, monkeypatch):
     torch.cuda.synchronize()
     taken, side = spied(sv, monkeypatch), torch.cuda.Stream()
     for i in range(len(want)):
-        call = calls[i] if i < len(calls) else lambda s: adapter(H.clone() if s is None else Y, s)
+        call = calls[i] if i < len(calls) else lambda s: adapter(Y if s is side else H.clone(), s)
         Y = H.clone()
         torch.cuda.synchronize()
         del taken[:]
         torch.cuda._sleep(200_000_000)
-        first, mine = call(None), list(taken)
+        first, mine = call(torch.cuda.current_stream()), list(taken)
         del taken[:]
         second = call(side)
         assert taken and not overlaps(mine, taken), i
