@@ -317,7 +317,9 @@ SVCONV_API size_t svconv_adapter_xattn_workspace_size(int T, int R, int chunk_T,
  *   without O's rounding, and O is not read)
  *     dQ = scale dS K,  dK = scale sum over the r query heads of dS^T Q,  dV = the same of P^T dO
  *   into dQ [nq][Hq][d], dK and dV [nkv][Hkv][d] bf16 (contiguous, overwritten; rows of dropped
- *   keys get 0).  Overlapping outputs are not allowed.  No atomics: deterministic.
+ *   keys get 0, whatever the rows of dO and Q hold).  The keys are those of the forward call, all of them: O and lse of a larger
+ *   set (a shard's keys with the whole set's lse) are not allowed.  Overlapping outputs are not allowed.  No atomics:
+ *   deterministic.
  */
 typedef struct {
   int nq, nkv;            /* rows of Q and of K / V */

@@ -1621,8 +1621,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_few_kernel(const __grid_
 
 // ---------------------------------------------------------------------------- backward, few keys
 // Groups of at most 96 keys (an encoder's states, a handful of landmarks) under many queries: the keys stay in shared
-// memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 42 us
-// against 76 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 93 against 147; 200 over 50: 14.5 against 12.4).
+// memory and the queries stream past them once, 5 products a tile (8 x 6,144 queries over 77 keys, 4 heads of 64: 43 us
+// against 77 by the two passes; 4 x 9,000 over 90, 8 heads of 128: 94 against 147; 1,000 over 50: 16.5 either way).  With fewer
+// queries the two passes are faster (200 over 50: 10.3 us against 14.4); this form is taken all the same, because it
+// rounds less (D, and dS up to kTwoKeys keys).
 //     S = Q K^T, dP = dO V^T;  dQ = dS K, written as it comes;  dV^T += dO^T P, dK^T += Q^T dS
 // A row's keys are all here, so D is the sum of P dP itself: no product with O, and none of its rounding, which would
 // show where few keys leave dP - D small.  With at most 64 keys dS goes into its products as two bf16 values, the
@@ -2122,9 +2124,10 @@ int cdiv(int a, int b) { return (int)(((long long)a + b - 1) / b); }
 
 // How a forward call is cut: pair or split form, and over how many splits of the keys.  The candidates are
 // compared by the time of whole rounds of CTAs over 148 SMs (a fixed number, so the workspace size needs no device
-// query), with the group lengths known only by their sum and bound.  In units of one key tile for both streams (about
-// 1.1 us): a tile costs 1 in the pair form and 1/2 in the split form, a CTA kFixed besides, and splits their
-// partial results.  Measured with 184 units of 64 key tiles of 128 channels: one split of the pair form 308 us.
+// query), with the group lengths known only by their sum and bound.  In units of one key tile for both streams (1.5 us
+// up to 64 channels, 1.9 at 128: 4,096 queries x 8 heads over 8,192 and 16,384 keys take 102 and 197 us, 132 and 254): a tile
+// costs 1 in the pair form and 1/2 in the split form, a CTA kFixed besides, and splits their partial results (kMerge and
+// kMergeBytes are the same at either width, so a merge counts for a quarter more at 128 channels).
 constexpr int kSms = 148, kMinTiles = 4;
 // Up to so many key tiles an item, CTAs loop over items.  24,576 queries x 4 heads of 64: 1 tile 26.7 us a CTA an item
 // and 20.6 us looping, 2 tiles 29.2 and 24.7, 4 tiles 37 and 37, 8 tiles 55 and 59; heads of 128, whose query tiles

@@ -5,7 +5,8 @@
 // (queries and keys) share one launch, split over the CTAs by their bytes.  A warp owns whole tokens: its
 // lanes form the sines and cosines of a token's pairs once and share them over all heads through shared
 // memory.  A head's d channels lie in d / 8 lanes (padded to a power of two), each lane holding both members
-// of its four pairs, so a norm is a few shuffles and a rotation none.  Four chunks per lane are in
+// of its four pairs, so a norm is a few shuffles and a rotation none.  Tokens of fewer than 256 channels in all leave lanes
+// idle: one head of 64 runs at a third of the bytes per second of four (1.3 and 4.1 TB/s forward).  Four chunks per lane are in
 // flight before the trigonometry starts.
 //
 // Angles: a pair's frequency in turns per position, formed in two doubles, is kept as a 64-bit binary fraction (off by
@@ -322,7 +323,9 @@ __device__ __forceinline__ void qk_tokens(const QkParams& p, const QkSide& side,
   }
 }
 
-// CTAs resident on an SM: as many as the registers of a variant allow without spills.
+// CTAs resident on an SM.  Two for the fp32 backward, whose registers allow no third without spills.  The bf16 backward
+// spills 150 to 280 bytes a thread at three: 112 us against 126 with two for 49,152 x 8 and 98,317 x 2 heads of 128 (interleaved),
+// 64 against 58 at 4 heads of 64, 124 against 111 at 80 (half).
 template <typename T, bool BWD>
 constexpr int kQkPerSm = BWD && sizeof(T) == 4 ? 2 : 3;
 

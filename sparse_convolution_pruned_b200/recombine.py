@@ -74,8 +74,8 @@ def recombine_fwd(Q, K, V, pos_q, pos_k, groups: Groups, rotation: Rotation, *, 
 
 
 def recombine_bwd(dO, saved: Saved, groups: Groups, rotation: Rotation, *, status=None, stream=None):
-    """(dQ, dK, dV bf16, dwq, dwk fp32 [d]) of recombine_fwd.  Rows of no group (a padded batch's) get zero
-    gradients; they and left-out keys add nothing to dwq and dwk as long as what they hold is finite."""
+    """(dQ, dK, dV bf16, dwq, dwk fp32 [d]) of recombine_fwd.  As long as what they hold is finite, rows of no group
+    (a padded batch's) get zero gradients, and they and left-out keys add nothing to dwq and dwk."""
     with torch.cuda.stream(stream):
         grads = [torch.zeros_like(t, memory_format=torch.contiguous_format) for t in (saved.Yq, saved.Yk, saved.V)]
     if stream is not None:  # that stream's memory, which the caller may use on the current one
